@@ -236,10 +236,118 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
                            int w0, int w_pretrained, double rope_theta, float scale,
                            jetlong_dtype dtype, void* stream);
 
+/* ---------------------------------------------------------------- paged cache
+ * For serving, the raw-key cache can be kept in pages:
+ *   kcache, vcache  [num_pages, Hkv, page_size, d], page_size 16, 32, 64, 128 or
+ *                   256 (else JETLONG_ERR_UNSUPPORTED);
+ *   block_table     int32 [B, max_pages]: entry p of request b is the page of its
+ *                   rows [p page_size, (p + 1) page_size); a page belongs to one
+ *                   request;
+ *   lens            int32 [B]: committed rows of each request.  Row r sits at
+ *                   position r.
+ * One step: jetlong_block_tables makes room for each request's new rows and gives
+ * their slots, jetlong_cache_append writes the rows, jetlong_decode_paged (one new
+ * row per request) or jetlong_decode_tree (a tree of drafted rows) attends, and
+ * the length advances by one, or by what jetlong_tree_commit accepts.  Lengths,
+ * tables and trees are device arrays, so a step can be captured into a CUDA graph
+ * and replayed as the requests grow.
+ *
+ * The host cannot check device arrays.  The kernels do: a value out of range is
+ * never followed, and the next jetlong_device_status returns
+ * JETLONG_ERR_INVALID_ARG (and clears the record).  int32 arrays must be 4-byte
+ * aligned, caches and rows 16-byte. */
+
+/* Block tables and slot maps from request lengths.  Request b holds held[b]
+ * pages (entries [0, held[b]) of its table row) for its lens[b] rows and takes
+ * grow[b] >= 0 more rows.  With release (may be NULL) and release[b] != 0 the
+ * request first gives all its pages back and starts again from length 0.
+ * free_list[0 .. *free_count) are the free pages (room for free_cap); pages are
+ * taken from its end, in request order.  Pages given back by this call go onto
+ * the list first (last request first, its last page first) and can be taken by
+ * it.  Writes
+ *   status[b]     0 granted; 1 refused, the free pages end here (a request that
+ *                 needs pages and comes after one is refused as well; one that
+ *                 needs none is granted); 2 refused, longer than its table row.
+ *                 A refused request keeps its pages;
+ *   lens_out[b]   lens[b], or 0 if released (the new rows are not counted);
+ *   held_out[b], *free_count_out, block_table entries [held, held_out);
+ *   row_start     [B + 1]: first of each request's rows in the step's token rows
+ *                 (the running sum of grow, refused requests included);
+ *   slot_map      [n_rows]: page * page_size + offset of every token row; -1 for
+ *                 refused requests and for rows from row_start[B] on.  n_rows
+ *                 must be at least row_start[B]; later rows are not written and
+ *                 device_status reports it.
+ * lens_out, held_out and free_count_out may be their inputs.  B <= 8192.  One
+ * launch, no workspace. */
+int jetlong_block_tables(const int32_t* lens, const int32_t* grow, const int32_t* release, const int32_t* held,
+                         const int32_t* free_count, int32_t* block_table, int32_t* free_list, int32_t* lens_out,
+                         int32_t* held_out, int32_t* free_count_out, int32_t* slot_map, int32_t* row_start,
+                         int32_t* status, int B, int max_pages, int page_size, int num_pages, int free_cap, int n_rows,
+                         void* stream);
+
+/* Writes raw key and value rows to their slots: row n, kv head h of k goes to
+ * kcache[slot / page_size][h][slot % page_size], slot = slot_map[n]; slot -1
+ * leaves the row out.  k, v: [N, Hkv, d] with d contiguous and any token and head
+ * strides (in elements, multiples of 16 bytes), e.g. slices of a fused
+ * projection, or [B, Hkv, L, d] prefill keys with token and head exchanged.
+ * Slots must differ from one another (those of jetlong_block_tables do).  N = 0
+ * does nothing. */
+int jetlong_cache_append(const void* k, const void* v, const int32_t* slot_map, void* kcache, void* vcache, int N,
+                         int Hkv, int d, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                         int64_t v_head_stride, int num_pages, int page_size, jetlong_dtype dtype, void* stream);
+
+/* Decode of one new row per request over the paged cache: q, out [B, Hq, d].  The
+ * caller has appended request b's new row as row lens[b]; it is the query's own
+ * row, at position lens[b], and G follows lens[b] + 1 (jetlong_decode with L =
+ * lens[b] + 1, each request with its own length).  A request with lens[b] < 0 is
+ * idle: its row of out is left as it was.  workspace: at least
+ * jetlong_decode_tree_workspace_size(B, Hq, Hkv, d, 1) bytes; its contents on
+ * entry do not matter, and calls that share it must not overlap on the device. */
+int jetlong_decode_paged(const void* q, const void* kcache, const void* vcache, void* out, const int32_t* block_table,
+                         const int32_t* lens, int B, int Hq, int Hkv, int d, int num_pages, int page_size,
+                         int max_pages, int w0, int w_pretrained, double rope_theta, float scale, jetlong_dtype dtype,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode of a tree of drafted rows per request (speculative decoding).  Request
+ * b's nodes are token rows [row_start[b], row_start[b + 1]) of q, out [N, Hq, d],
+ * at most max_nodes <= 64 of them; node t has been appended as cache row lens[b] +
+ * t.  parents[row] is the node's parent within its request, smaller than the node
+ * itself, or -1 for a child of the last committed row; parents NULL: a chain.
+ * Node t at depth e(t) has position i = lens[b] + e(t) and G from i + 1; it
+ * attends the committed rows and its ancestors and itself, at their positions
+ * -- what jetlong_decode gives after its path has been committed.
+ * Values in rows a node does not attend (non-finite ones too) do not reach it.
+ * Requests may have no nodes; token rows outside every request are left as they
+ * were.  Without row_start (NULL) every request has one node, row b:
+ * jetlong_decode_paged.
+ * Two launches: the attention, cut into equal pieces over all requests whatever
+ * their lengths, and a merge of the cut ones.  bf16 takes the input range of
+ * jetlong_decode. */
+size_t jetlong_decode_tree_workspace_size(int B, int Hq, int Hkv, int d, int max_nodes);
+int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, void* out, const int32_t* block_table,
+                        const int32_t* lens, const int32_t* row_start, const int32_t* parents, int B, int N, int Hq,
+                        int Hkv, int d, int num_pages, int page_size, int max_pages, int max_nodes, int w0,
+                        int w_pretrained, double rope_theta, float scale, jetlong_dtype dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Commits the accepted part of a draft: last[b] is the deepest accepted node of
+ * request b (-1: none).  Its ancestors and itself, path[0..n), become rows lens[b]
+ * .. lens[b] + n - 1 (row lens[b] + path[j] is copied to row lens[b] + j; raw rows
+ * need no new rotation), lens_out[b] = lens[b] + n (lens_out may be lens) and,
+ * unless NULL, n_accepted[b] = n.  The remaining drafted rows are left where they
+ * are, behind the new length.  row_start, parents, N, max_nodes as in
+ * jetlong_decode_tree. */
+int jetlong_tree_commit(void* kcache, void* vcache, const int32_t* block_table, const int32_t* lens,
+                        const int32_t* row_start, const int32_t* parents, const int32_t* last, int32_t* lens_out,
+                        int32_t* n_accepted, int B, int N, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                        int max_nodes, jetlong_dtype dtype, void* stream);
+
 /* Synchronises `stream`, then reads and clears the library's device error
  * word, set by a kernel whose bounded wait expired (the kernel then returned
- * without finishing its tile).  Returns JETLONG_OK, JETLONG_ERR_TIMEOUT or
- * JETLONG_ERR_CUDA. */
+ * without finishing its tile), and, if that is clear, the input word of the
+ * paged-cache calls (set by a kernel that met an out-of-range value in a device
+ * array).  Returns JETLONG_OK, JETLONG_ERR_TIMEOUT, JETLONG_ERR_INVALID_ARG (a
+ * device array) or JETLONG_ERR_CUDA. */
 int jetlong_device_status(void* stream);
 
 /* Self test of the failure-detection path (the pages have no counterpart):

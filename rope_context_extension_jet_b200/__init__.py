@@ -18,6 +18,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 __all__ = [
     "BF16", "FP32", "JetLongError", "load_library", "group_size", "position_map", "prefill",
@@ -25,6 +26,8 @@ __all__ = [
     "decode", "decode_rope_cache", "decode_noalloc", "device_status", "last_error", "launch_count",
     "DECODE_NOALLOC_SCRATCH_BYTES", "selftest_wait_timeout", "debug_inject_timeout",
     "INJECT_PREFILL_KEY_TILE", "INJECT_DECODE_COPY", "debug_rope_phase", "debug_tile_plan", "debug_ex2", "debug_rope_keys",
+    "BlockTables", "block_tables", "cache_append", "decode_tree_workspace_size", "decode_paged", "decode_tree",
+    "tree_commit",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -99,6 +102,18 @@ def load_library(path: str | None = None):
         lib.jetlong_debug_ex2.argtypes = [vp, i64, vp, vp]
         lib.jetlong_debug_rope_keys.restype = i32
         lib.jetlong_debug_rope_keys.argtypes = [vp, i32, i32, i32, i32, dbl, vp, vp, ctypes.POINTER(ctypes.c_int), vp]
+        lib.jetlong_block_tables.restype = i32
+        lib.jetlong_block_tables.argtypes = [vp] * 13 + [i32] * 6 + [vp]
+        lib.jetlong_cache_append.restype = i32
+        lib.jetlong_cache_append.argtypes = [vp] * 5 + [i32] * 3 + [i64] * 4 + [i32] * 3 + [vp]
+        lib.jetlong_decode_tree_workspace_size.restype = sz
+        lib.jetlong_decode_tree_workspace_size.argtypes = [i32] * 5
+        lib.jetlong_decode_paged.restype = i32
+        lib.jetlong_decode_paged.argtypes = [vp] * 6 + [i32] * 9 + [dbl, flt, i32, vp, sz, vp]
+        lib.jetlong_decode_tree.restype = i32
+        lib.jetlong_decode_tree.argtypes = [vp] * 8 + [i32] * 11 + [dbl, flt, i32, vp, sz, vp]
+        lib.jetlong_tree_commit.restype = i32
+        lib.jetlong_tree_commit.argtypes = [vp] * 9 + [i32] * 9 + [vp]
         lib.jetlong_device_status.restype = i32
         lib.jetlong_device_status.argtypes = [vp]
         lib.jetlong_last_error.restype = ctypes.c_char_p
@@ -387,6 +402,175 @@ def decode_noalloc(q, kcache, vcache, L: int, out=None, *, w0: int, w_pretrained
                                       int(w_pretrained), float(rope_theta), float(scale),
                                       _dtype_code(q), _stream(stream)), lib)
     return out
+
+
+# ---------------------------------------------------------------- paged cache
+# kcache, vcache [num_pages, Hkv, page_size, d]; block_table int32 [B, max_pages];
+# lens int32 [B] committed rows per request.  All arrays live on the device, so a
+# step (block_tables, cache_append, decode_paged or decode_tree, tree_commit) can
+# be captured into a CUDA graph.
+
+def _ints(t, name, shape, optional=False):
+    """Device pointer of an int32 array of the given shape (None where optional)."""
+    import torch
+    if t is None and optional:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be an int32 tensor of shape {tuple(shape)} (got {t.dtype}, {tuple(t.shape)})")
+    return _dev(t, name)
+
+
+def _caches(kcache, vcache):
+    if kcache.dim() != 4 or vcache.shape != kcache.shape:
+        raise ValueError("kcache and vcache must both be [num_pages, Hkv, page_size, d]")
+    _same_dtype((kcache, "kcache"), (vcache, "vcache"))
+    return kcache.shape
+
+
+class BlockTables(NamedTuple):
+    """Result of ``block_tables`` (int32 CUDA tensors; the block table and the free list are updated in place)."""
+    lens: "object"        # [B] committed rows (0 for released requests)
+    held: "object"        # [B] pages held
+    free_count: "object"  # [1] free pages left
+    slot_map: "object"    # [n_rows] slot of every new row, -1: none
+    row_start: "object"   # [B + 1] first token row of each request
+    status: "object"      # [B] 0 granted, 1 no free pages, 2 longer than its table row
+
+
+def block_tables(lens, grow, block_table, held, free_list, free_count, *, page_size: int, num_pages: int, n_rows: int,
+                 release=None, lens_out=None, held_out=None, free_count_out=None, slot_map=None, row_start=None,
+                 status=None, stream=None) -> BlockTables:
+    """Make room for grow[b] new rows of every request and map them to slots
+    (jetlong_block_tables).  ``block_table`` [B, max_pages] and ``free_list`` are
+    updated in place; the ``*_out`` arrays may be their inputs."""
+    import torch
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and free_list one-dimensional")
+    B, max_pages = block_table.shape
+    i32, dev = torch.int32, block_table.device
+    lens_out = torch.empty(B, dtype=i32, device=dev) if lens_out is None else lens_out
+    held_out = torch.empty(B, dtype=i32, device=dev) if held_out is None else held_out
+    free_count_out = torch.empty(1, dtype=i32, device=dev) if free_count_out is None else free_count_out
+    slot_map = torch.empty(n_rows, dtype=i32, device=dev) if slot_map is None else slot_map
+    row_start = torch.empty(B + 1, dtype=i32, device=dev) if row_start is None else row_start
+    status = torch.empty(B, dtype=i32, device=dev) if status is None else status
+    lib = load_library()
+    _check(lib.jetlong_block_tables(
+        _ints(lens, "lens", (B,)), _ints(grow, "grow", (B,)), _ints(release, "release", (B,), True),
+        _ints(held, "held", (B,)), _ints(free_count, "free_count", (1,)),
+        _ints(block_table, "block_table", (B, max_pages)), _ints(free_list, "free_list", (free_list.shape[0],)),
+        _ints(lens_out, "lens_out", (B,)), _ints(held_out, "held_out", (B,)),
+        _ints(free_count_out, "free_count_out", (1,)), _ints(slot_map, "slot_map", (n_rows,)),
+        _ints(row_start, "row_start", (B + 1,)), _ints(status, "status", (B,)), B, max_pages, int(page_size),
+        int(num_pages), free_list.shape[0], int(n_rows), _stream(stream)), lib)
+    return BlockTables(lens_out, held_out, free_count_out, slot_map, row_start, status)
+
+
+def _rows(t, name, like, N):
+    """Pointer and (token, head) strides of a [N, Hkv, d] tensor whose rows are contiguous."""
+    import torch
+    _, Hkv, _, d = like.shape
+    if tuple(t.shape) != (N, Hkv, d) or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be [N, Hkv, d] = {(N, Hkv, d)} with the cache's dtype (got {tuple(t.shape)}, {t.dtype})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device} but the library runs on the current device "
+                         f"cuda:{torch.cuda.current_device()} (select it with torch.cuda.device)")
+    if t.stride(2) != 1 and N > 0:
+        raise ValueError(f"{name} must have contiguous rows (stride 1 in d)")
+    # the stride of a dimension of size one is arbitrary and unused
+    return t.data_ptr(), t.stride(0) if N > 1 else 0, t.stride(1) if Hkv > 1 else 0
+
+
+def cache_append(k, v, slot_map, kcache, vcache, stream=None):
+    """Write raw rows k, v [N, Hkv, d] (any token and head strides) to their
+    slots of the paged cache; slot -1 leaves a row out (jetlong_cache_append)."""
+    num_pages, Hkv, page_size, d = _caches(kcache, vcache)
+    N = k.shape[0]
+    lib = load_library()
+    kp, kt, kh = _rows(k, "k", kcache, N)
+    vp, vt, vh = _rows(v, "v", kcache, N)
+    _check(lib.jetlong_cache_append(kp, vp, _ints(slot_map, "slot_map", (N,)), _dev(kcache, "kcache"),
+                                    _dev(vcache, "vcache"), N, Hkv, d, kt, kh, vt, vh, num_pages, page_size,
+                                    _dtype_code(kcache), _stream(stream)), lib)
+
+
+def decode_tree_workspace_size(B: int, Hq: int, Hkv: int, d: int, max_nodes: int = 1) -> int:
+    return int(load_library().jetlong_decode_tree_workspace_size(B, Hq, Hkv, d, max_nodes))
+
+
+def _paged_shapes(q, kcache, vcache, block_table):
+    num_pages, Hkv, page_size, d = _caches(kcache, vcache)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [N, Hq, d] with the cache's d")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    _same_dtype((q, "q"), (kcache, "kcache"), (vcache, "vcache"))
+    return num_pages, Hkv, page_size, d
+
+
+def decode_paged(q, kcache, vcache, block_table, lens, out=None, *, w0: int, w_pretrained: int, rope_theta: float,
+                 scale: float | None = None, workspace=None, stream=None):
+    """One decode step of every request over the paged cache: raw q [B, Hq, d],
+    request b's query (and its own row) at position lens[b]; requests with
+    lens[b] < 0 are idle and their rows of ``out`` untouched (jetlong_decode_paged)."""
+    return decode_tree(q, kcache, vcache, block_table, lens, None, None, out, max_nodes=1, w0=w0,
+                       w_pretrained=w_pretrained, rope_theta=rope_theta, scale=scale, workspace=workspace,
+                       stream=stream)
+
+
+def decode_tree(q, kcache, vcache, block_table, lens, row_start, parents=None, out=None, *, max_nodes: int, w0: int,
+                w_pretrained: int, rope_theta: float, scale: float | None = None, workspace=None, stream=None):
+    """Decode a tree of drafted rows per request: raw q [N, Hq, d], request b's
+    nodes in token rows [row_start[b], row_start[b + 1]), parents [N] within each
+    request (-1: the last committed row; None: chains), node t appended as row
+    lens[b] + t (jetlong_decode_tree)."""
+    import torch
+    num_pages, Hkv, page_size, d = _paged_shapes(q, kcache, vcache, block_table)
+    N, Hq, _ = q.shape
+    B, max_pages = block_table.shape
+    if row_start is None and N != B:
+        raise ValueError("without row_start, q must have one row per request")
+    if out is None:
+        out = torch.empty_like(q)
+    _like(out, q, "out", "q")
+    lib = load_library()
+    if workspace is None:
+        workspace = torch.empty(decode_tree_workspace_size(B, Hq, Hkv, d, int(max_nodes)), dtype=torch.uint8,
+                                device=q.device)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    _check(lib.jetlong_decode_tree(
+        _dev(q, "q"), _dev(kcache, "kcache"), _dev(vcache, "vcache"), _dev(out, "out"),
+        _ints(block_table, "block_table", (B, max_pages)), _ints(lens, "lens", (B,)),
+        _ints(row_start, "row_start", (B + 1,), True), _ints(parents, "parents", (N,), True), B, N, Hq, Hkv, d,
+        num_pages, page_size, max_pages, int(max_nodes), int(w0), int(w_pretrained), float(rope_theta), float(scale),
+        _dtype_code(q), _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream)), lib)
+    return out
+
+
+def tree_commit(kcache, vcache, block_table, lens, row_start, parents, last, *, max_nodes: int, lens_out=None,
+                n_accepted=None, stream=None):
+    """Commit the path to node last[b] (-1: none) of every request: its rows
+    become rows lens[b], lens[b] + 1, ... and lens_out = lens + their number
+    (jetlong_tree_commit).  Returns (lens_out, n_accepted)."""
+    import torch
+    num_pages, Hkv, page_size, d = _caches(kcache, vcache)
+    if block_table.dim() != 2 or row_start.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and row_start [B + 1]")
+    B, max_pages = block_table.shape
+    lens_out = torch.empty_like(lens) if lens_out is None else lens_out
+    n_accepted = torch.empty_like(lens) if n_accepted is None else n_accepted
+    # without parents (chains) the token rows are not read and need no bound
+    N = 2147483647 if parents is None else parents.numel()
+    lib = load_library()
+    _check(lib.jetlong_tree_commit(
+        _dev(kcache, "kcache"), _dev(vcache, "vcache"), _ints(block_table, "block_table", (B, max_pages)),
+        _ints(lens, "lens", (B,)), _ints(row_start, "row_start", (B + 1,)), _ints(parents, "parents", (N,), True),
+        _ints(last, "last", (B,)), _ints(lens_out, "lens_out", (B,)), _ints(n_accepted, "n_accepted", (B,)), B, N,
+        Hkv, d, num_pages, page_size, max_pages, int(max_nodes), _dtype_code(kcache), _stream(stream)), lib)
+    return lens_out, n_accepted
 
 
 def selftest_wait_timeout(stream=None):

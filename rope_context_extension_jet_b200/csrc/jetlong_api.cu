@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "jl_common.cuh"
+#include "paged_common.cuh"
 
 namespace {
 
@@ -43,6 +44,10 @@ void take_injection(int* site, long long* cycles)
     g_inject_cycles = 0;
 }
 __device__ int g_dev_error;  // set by kernels whose bounded waits expire
+// set by the paged-cache kernels when a value in device memory (a page number, a
+// slot, a length, a parent) is out of range; kept apart from g_dev_error, which
+// later launches look at
+__device__ int g_input_error;
 
 int fail(int code, const char* fmt, ...)
 {
@@ -72,6 +77,23 @@ int* dev_error_word(cudaError_t* err)
     if (!cache[dev]) {
         void* p = nullptr;
         *err = cudaGetSymbolAddress(&p, g_dev_error);
+        if (*err != cudaSuccess) return nullptr;
+        cache[dev] = static_cast<int*>(p);
+    }
+    return cache[dev];
+}
+
+int* input_error_word(cudaError_t* err)
+{
+    static std::mutex mu;
+    static int* cache[64] = {nullptr};
+    int dev = 0;
+    *err = cudaGetDevice(&dev);
+    if (*err != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!cache[dev]) {
+        void* p = nullptr;
+        *err = cudaGetSymbolAddress(&p, g_input_error);
         if (*err != cudaSuccess) return nullptr;
         cache[dev] = static_cast<int*>(p);
     }
@@ -750,7 +772,219 @@ int jetlong_device_status(void* stream)
         cudaMemcpy(derr, &z, sizeof z, cudaMemcpyHostToDevice);
         return fail(JETLONG_ERR_TIMEOUT, "a bounded device wait expired (code 0x%x)", h);
     }
+    int* ierr = input_error_word(&e);
+    if (!ierr) return fail(JETLONG_ERR_CUDA, "device input word: %s", cudaGetErrorString(e));
+    e = cudaMemcpy(&h, ierr, sizeof h, cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return fail(JETLONG_ERR_CUDA, "read input word: %s", cudaGetErrorString(e));
+    if (h != 0) {
+        int z = 0;
+        cudaMemcpy(ierr, &z, sizeof z, cudaMemcpyHostToDevice);
+        const char* what = h == jl::kBadPage       ? "a page number outside the cache"
+                           : h == jl::kBadSlot     ? "a slot outside the cache"
+                           : h == jl::kBadLength   ? "a length that is negative or exceeds its block table"
+                           : h == jl::kBadRows     ? "row_start or the row count does not fit the token rows"
+                           : h == jl::kBadParent   ? "a node or parent index out of order"
+                           : h == jl::kBadFreeList ? "free_count or a returned page does not fit the free list"
+                                                   : "unknown";
+        return fail(JETLONG_ERR_INVALID_ARG, "out-of-range value in device memory: %s (code 0x%x)", what, h);
+    }
     return ok();
+}
+
+// ---------------------------------------------------------------------------
+// Paged cache.
+
+static int check_pages(int num_pages, int page_size, int max_pages, int* shift)
+{
+    if (num_pages < 1 || max_pages < 1)
+        return fail(JETLONG_ERR_INVALID_ARG, "need num_pages >= 1 and max_pages >= 1 (got %d, %d)", num_pages, max_pages);
+    int sh = 0;
+    while (sh < 30 && (1 << sh) < page_size) ++sh;
+    if (page_size < 16 || page_size > 256 || (1 << sh) != page_size)
+        return fail(JETLONG_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256 (got %d)", page_size);
+    if ((int64_t)num_pages * page_size > 2147483647LL || (int64_t)max_pages * page_size > 2147482623LL)
+        return fail(JETLONG_ERR_UNSUPPORTED, "num_pages * page_size and max_pages * page_size must fit 31 bits");
+    *shift = sh;
+    return JETLONG_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int jetlong_block_tables(const int32_t* lens, const int32_t* grow, const int32_t* release, const int32_t* held,
+                         const int32_t* free_count, int32_t* block_table, int32_t* free_list, int32_t* lens_out,
+                         int32_t* held_out, int32_t* free_count_out, int32_t* slot_map, int32_t* row_start,
+                         int32_t* status, int B, int max_pages, int page_size, int num_pages, int free_cap, int n_rows,
+                         void* stream)
+{
+    if (!lens || !grow || !held || !free_count || !block_table || !free_list || !lens_out || !held_out ||
+        !free_count_out || !row_start || !status || (n_rows > 0 && !slot_map))
+        return fail(JETLONG_ERR_INVALID_ARG, "null pointer argument");
+    const void* all[] = {lens, grow, release, held, free_count, block_table, free_list, lens_out, held_out,
+                         free_count_out, slot_map, row_start, status};
+    for (const void* x : all)
+        if (!aligned4(x)) return fail(JETLONG_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+    if (B < 1 || n_rows < 0 || free_cap < 1)
+        return fail(JETLONG_ERR_INVALID_ARG, "need B >= 1, n_rows >= 0, free_cap >= 1 (got %d, %d, %d)", B, n_rows, free_cap);
+    if (B > jl::kMaxTableRequests)
+        return fail(JETLONG_ERR_UNSUPPORTED, "B must be <= %d (got %d)", jl::kMaxTableRequests, B);
+    jl::TablesProblem p{};
+    int st = check_pages(num_pages, page_size, max_pages, &p.page_shift);
+    if (st != JETLONG_OK) return st;
+    if ((int64_t)B * max_pages > 2147483647LL)
+        return fail(JETLONG_ERR_UNSUPPORTED, "B * max_pages must fit 31 bits");
+    cudaError_t e;
+    p.input_error = input_error_word(&e);
+    if (!p.input_error) return fail(JETLONG_ERR_CUDA, "device input word: %s", cudaGetErrorString(e));
+    p.lens = lens; p.grow = grow; p.release = release; p.held = held; p.free_count = free_count;
+    p.table = block_table; p.free_list = free_list; p.lens_out = lens_out; p.held_out = held_out;
+    p.free_count_out = free_count_out; p.slot_map = slot_map; p.row_start = row_start; p.status = status;
+    p.B = B; p.max_pages = max_pages; p.page_size = page_size; p.num_pages = num_pages; p.free_cap = free_cap;
+    p.n_rows = n_rows;
+    int n = 0;
+    e = jl::launch_block_tables(p, (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return fail(JETLONG_ERR_CUDA, "block tables launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+static int check_row(int Hkv, int d, jetlong_dtype dtype, int* row_bytes)
+{
+    if (Hkv < 1) return fail(JETLONG_ERR_INVALID_ARG, "Hkv must be positive (got %d)", Hkv);
+    if (dtype != JETLONG_BF16 && dtype != JETLONG_FP32)
+        return fail(JETLONG_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (d != 64 && d != 128)
+        return fail(JETLONG_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
+    if (Hkv > 65535) return fail(JETLONG_ERR_UNSUPPORTED, "Hkv must be <= 65535");
+    *row_bytes = d * (dtype == JETLONG_FP32 ? 4 : 2);
+    return JETLONG_OK;
+}
+
+int jetlong_cache_append(const void* k, const void* v, const int32_t* slot_map, void* kcache, void* vcache, int N,
+                         int Hkv, int d, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                         int64_t v_head_stride, int num_pages, int page_size, jetlong_dtype dtype, void* stream)
+{
+    if (N < 0) return fail(JETLONG_ERR_INVALID_ARG, "N must be >= 0 (got %d)", N);
+    jl::AppendProblem p{};
+    int st = check_row(Hkv, d, dtype, &p.row_bytes);
+    if (st == JETLONG_OK) st = check_pages(num_pages, page_size, 1, &p.page_shift);
+    if (st != JETLONG_OK) return st;
+    if (N == 0) return ok();
+    if (!k || !v || !slot_map || !kcache || !vcache) return fail(JETLONG_ERR_INVALID_ARG, "null pointer argument");
+    const int64_t el = dtype == JETLONG_FP32 ? 4 : 2;
+    const int64_t strides[] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+    bool ok16 = aligned16(k) && aligned16(v) && aligned16(kcache) && aligned16(vcache);
+    for (int64_t x : strides) ok16 = ok16 && (x * el) % 16 == 0;
+    if (!ok16 || !aligned4(slot_map))
+        return fail(JETLONG_ERR_INVALID_ARG, "rows and caches must be 16-byte aligned (strides included)");
+    cudaError_t e;
+    p.input_error = input_error_word(&e);
+    if (!p.input_error) return fail(JETLONG_ERR_CUDA, "device input word: %s", cudaGetErrorString(e));
+    p.k = k; p.v = v; p.slots = slot_map; p.kc = kcache; p.vc = vcache;
+    p.N = N; p.Hkv = Hkv;
+    p.k_token = k_token_stride * el; p.k_head = k_head_stride * el;
+    p.v_token = v_token_stride * el; p.v_head = v_head_stride * el;
+    p.num_pages = num_pages; p.page_size = page_size;
+    int n = 0;
+    e = jl::launch_cache_append(p, (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return fail(JETLONG_ERR_CUDA, "cache append launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+int jetlong_tree_commit(void* kcache, void* vcache, const int32_t* block_table, const int32_t* lens,
+                        const int32_t* row_start, const int32_t* parents, const int32_t* last, int32_t* lens_out,
+                        int32_t* n_accepted, int B, int N, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                        int max_nodes, jetlong_dtype dtype, void* stream)
+{
+    if (!kcache || !vcache || !block_table || !lens || !row_start || !last || !lens_out)
+        return fail(JETLONG_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(kcache) || !aligned16(vcache))
+        return fail(JETLONG_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+    const void* all[] = {block_table, lens, row_start, parents, last, lens_out, n_accepted};
+    for (const void* x : all)
+        if (!aligned4(x)) return fail(JETLONG_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+    if (B < 1 || N < 0) return fail(JETLONG_ERR_INVALID_ARG, "need B >= 1 and N >= 0 (got %d, %d)", B, N);
+    if (max_nodes < 1 || max_nodes > jl::kMaxNodes)
+        return fail(JETLONG_ERR_INVALID_ARG, "max_nodes must be in [1, %d] (got %d)", jl::kMaxNodes, max_nodes);
+    jl::CommitProblem p{};
+    int st = check_row(Hkv, d, dtype, &p.row_bytes);
+    if (st == JETLONG_OK) st = check_pages(num_pages, page_size, max_pages, &p.page_shift);
+    if (st != JETLONG_OK) return st;
+    cudaError_t e;
+    p.input_error = input_error_word(&e);
+    if (!p.input_error) return fail(JETLONG_ERR_CUDA, "device input word: %s", cudaGetErrorString(e));
+    p.kc = kcache; p.vc = vcache; p.table = block_table; p.lens = lens; p.row_start = row_start;
+    p.parents = parents; p.last = last; p.lens_out = lens_out; p.n_accepted = n_accepted;
+    p.B = B; p.N = N; p.Hkv = Hkv; p.num_pages = num_pages; p.page_size = page_size; p.max_pages = max_pages;
+    p.max_nodes = max_nodes;
+    int n = 0;
+    e = jl::launch_tree_commit(p, (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return fail(JETLONG_ERR_CUDA, "tree commit launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+size_t jetlong_decode_tree_workspace_size(int B, int Hq, int Hkv, int d, int max_nodes)
+{
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (d != 64 && d != 128)) return 0;
+    if (max_nodes < 1 || max_nodes > jl::kMaxNodes) return 0;
+    return jl::paged_workspace_bytes(B, Hq, Hkv, d, max_nodes);
+}
+
+int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, void* out, const int32_t* block_table,
+                        const int32_t* lens, const int32_t* row_start, const int32_t* parents, int B, int N, int Hq,
+                        int Hkv, int d, int num_pages, int page_size, int max_pages, int max_nodes, int w0,
+                        int w_pretrained, double rope_theta, float scale, jetlong_dtype dtype, void* workspace,
+                        size_t workspace_bytes, void* stream)
+{
+    if (N < 0) return fail(JETLONG_ERR_INVALID_ARG, "N must be >= 0 (got %d)", N);
+    if (!kcache || !vcache || !block_table || !lens || !workspace || (N > 0 && (!q || !out)))
+        return fail(JETLONG_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(out) || !aligned16(workspace))
+        return fail(JETLONG_ERR_INVALID_ARG, "tensors, caches and workspace must be 16-byte aligned");
+    if (!aligned4(block_table) || !aligned4(lens) || !aligned4(row_start) || !aligned4(parents))
+        return fail(JETLONG_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+    int st = check_common(B, Hq, Hkv, d, w0, w_pretrained, rope_theta, scale, dtype);
+    if (st != JETLONG_OK) return st;
+    if (max_nodes < 1 || max_nodes > jl::kMaxNodes)
+        return fail(JETLONG_ERR_INVALID_ARG, "max_nodes must be in [1, %d] (got %d)", jl::kMaxNodes, max_nodes);
+    if (!row_start && (N != B || max_nodes != 1 || parents))
+        return fail(JETLONG_ERR_INVALID_ARG, "without row_start each request has one node: N = B, max_nodes = 1, no parents");
+    jl::PagedProblem p{};
+    st = check_pages(num_pages, page_size, max_pages, &p.page_shift);
+    if (st != JETLONG_OK) return st;
+    const size_t need = jl::paged_workspace_bytes(B, Hq, Hkv, d, max_nodes);
+    if (workspace_bytes < need)
+        return fail(JETLONG_ERR_INVALID_ARG, "workspace too small (%zu < %zu bytes)", workspace_bytes, need);
+    if (N == 0) return ok();
+    cudaError_t e;
+    p.dev_error = dev_error_word(&e);
+    if (!p.dev_error) return fail(JETLONG_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
+    p.input_error = input_error_word(&e);
+    if (!p.input_error) return fail(JETLONG_ERR_CUDA, "device input word: %s", cudaGetErrorString(e));
+    p.q = q; p.kc = kcache; p.vc = vcache; p.out = out;
+    p.table = block_table; p.lens = lens; p.row_start = row_start; p.parents = parents;
+    p.B = B; p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.group = Hq / Hkv;
+    p.num_pages = num_pages; p.page_size = page_size; p.max_pages = max_pages; p.max_nodes = max_nodes;
+    p.w0 = w0; p.w_pre = w_pretrained;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    jl::make_rope_turns(&p.turns, d, rope_theta);
+    p.workspace = static_cast<unsigned char*>(workspace);
+    int n = 0;
+    e = jl::launch_decode_paged(p, d, dtype, (cudaStream_t)stream, &n);
+    g_launches += n;
+    if (e != cudaSuccess) return fail(JETLONG_ERR_CUDA, "paged decode launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+int jetlong_decode_paged(const void* q, const void* kcache, const void* vcache, void* out, const int32_t* block_table,
+                         const int32_t* lens, int B, int Hq, int Hkv, int d, int num_pages, int page_size,
+                         int max_pages, int w0, int w_pretrained, double rope_theta, float scale, jetlong_dtype dtype,
+                         void* workspace, size_t workspace_bytes, void* stream)
+{
+    return jetlong_decode_tree(q, kcache, vcache, out, block_table, lens, nullptr, nullptr, B, B, Hq, Hkv, d, num_pages,
+                               page_size, max_pages, 1, w0, w_pretrained, rope_theta, scale, dtype, workspace,
+                               workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,277 @@
+// paged_common.cuh -- shared by the paged-cache operators: problem descriptions,
+// the codes of the device input word, and the work plan of the paged decode.
+//
+// Cache layout: pages [num_pages][Hkv][page_size][d]; table[b][p] is the page
+// that holds rows [p page_size, (p + 1) page_size) of request b.  Row lengths
+// and page numbers live on the device (no host copy is needed to launch), so
+// what the host cannot check is checked by the kernels: an out-of-range value
+// is never followed, its request or row is left out, and a code is recorded in
+// the device input word that jetlong_device_status reports.
+#pragma once
+
+#include "jl_common.cuh"
+
+namespace jl {
+
+constexpr int kMaxNodes = 64;  // drafted tokens per request: ancestors fit one 64-bit mask
+
+constexpr int kMaxTableRequests = 8192;  // block_tables: 5 words of shared memory per request
+
+// Codes of the device input word.
+enum {
+    kBadPage = 0x201,     // a page number outside [0, num_pages)
+    kBadSlot = 0x202,     // a slot outside [-1, num_pages * page_size)
+    kBadLength = 0x203,   // a negative length, or rows beyond the block table
+    kBadRows = 0x204,     // row_start decreasing, outside the token rows, or more than max_nodes apart
+    kBadParent = 0x205,   // a parent that does not precede its node
+    kBadFreeList = 0x206, // free_count outside the list, or more pages given back than it holds
+};
+
+struct PagedProblem {
+    const void *q, *kc, *vc;
+    void* out;
+    const int *table, *lens, *row_start, *parents;  // row_start / parents may be null
+    int B, N, Hq, Hkv, group;
+    int num_pages, page_size, page_shift, max_pages, max_nodes;
+    int w0, w_pre;
+    float scale_log2;
+    RopeTurns turns;
+    unsigned char* workspace;
+    int* input_error;
+    int* dev_error;
+};
+
+struct TablesProblem {
+    const int *lens, *grow, *release, *held, *free_count;
+    int *table, *free_list, *lens_out, *held_out, *free_count_out, *slot_map, *row_start, *status;
+    int B, max_pages, page_size, page_shift, num_pages, free_cap, n_rows;
+    int* input_error;
+};
+
+struct AppendProblem {
+    const void *k, *v;
+    const int* slots;
+    void *kc, *vc;
+    int N, Hkv, row_bytes;               // row_bytes = d * element size
+    long long k_token, k_head, v_token, v_head;  // input strides in bytes
+    int num_pages, page_size, page_shift;
+    int* input_error;
+};
+
+struct CommitProblem {
+    void *kc, *vc;
+    const int *table, *lens, *row_start, *parents, *last;
+    int *lens_out, *n_accepted;
+    int B, N, Hkv, row_bytes, num_pages, page_size, page_shift, max_pages, max_nodes;
+    int* input_error;
+};
+
+cudaError_t launch_block_tables(const TablesProblem& p, cudaStream_t s, int* nlaunch);
+cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t s, int* nlaunch);
+cudaError_t launch_tree_commit(const CommitProblem& p, cudaStream_t s, int* nlaunch);
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_nodes);
+cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch);
+
+__device__ __forceinline__ void record_input(int* word, int code)
+{
+    if (word) atomicCAS(word, 0, code);
+}
+
+#ifdef __CUDACC__
+
+// ---------------------------------------------------------------------------
+// Work plan of the paged decode.
+//
+// One unit = (request, kv head, tile of RT query rows); query row r of a
+// request is node r / group, head r % group of the kv head.  A unit visits its
+// keys in tiles of KT as a list of items: for every group size g its nodes can
+// have, the tiles that can hold remote pairs (rotated to floor(x / g)), then
+// the tiles that can hold local pairs (exact positions).  A tile on the border
+// is visited in both with complementary masks, so one online softmax takes
+// both branches.  With g = 1 throughout both rotations agree and every pair
+// counts as local.
+//
+// All items of all units form one line, cut into equal pieces of `per` items,
+// one per CTA: no CTA waits for the longest request.  A unit that lies in one
+// piece is written out at once; the pieces of the others leave partial softmax
+// states in the workspace (slot 2 c for the piece of CTA c that continues a
+// unit, 2 c + 1 for one that begins it) for the merge kernel.
+struct SeqPlan {
+    int L, T;        // committed rows and nodes (T = 0: nothing to do)
+    int n0;          // first token row
+    int gmin, ng;    // group sizes gmin .. gmin + ng - 1 have remote phases (ng may be 0)
+    int nR;          // tiles [0, nR) of each remote phase
+    int kE0, n;      // tiles [kE0, n) of the exact phase
+    int w0;          // window (INT_MAX when g = 1 throughout)
+    int items;       // per unit
+    int row_tiles;
+};
+
+template <int KT, int RT>
+__device__ inline SeqPlan seq_plan(const PagedProblem& p, int b, bool report)
+{
+    SeqPlan s;
+    int L = p.lens[b], a = b, T = L >= 0 ? 1 : 0;
+    int bad = 0;
+    if (p.row_start) {
+        a = p.row_start[b];
+        T = p.row_start[b + 1] - a;
+        if (a < 0 || T < 0 || T > p.max_nodes || a > p.N - T) {
+            bad = kBadRows;
+            T = 0;
+        } else if (T > 0 && L < 0) {
+            bad = kBadLength;
+        }
+    }
+    if (T > 0 && (long long)L + T > (long long)p.max_pages * p.page_size) bad = kBadLength;
+    if (bad) {
+        if (report) record_input(p.input_error, bad);
+        T = 0;
+    }
+    s.L = L;
+    s.T = T;
+    s.n0 = a;
+    if (T == 0) {
+        s.gmin = 1;
+        s.ng = s.nR = s.kE0 = s.n = s.items = s.row_tiles = 0;
+        s.w0 = 0;
+        return s;
+    }
+    const int imax = L + T - 1;  // no node is deeper than T - 1
+    const int g0 = L / p.w_pre + 1, g1 = imax / p.w_pre + 1;
+    s.n = (L + T + KT - 1) / KT;
+    s.gmin = g0;
+    s.w0 = p.w0;
+    if (g1 == 1) s.w0 = 0x7fffffff;
+    // a tile can hold remote pairs if its smallest position is at most imax - w0
+    // (drafted rows sit at positions >= L whatever their row)
+    const int far = imax - s.w0;  // may be negative
+    s.nR = far < 0 ? 0 : (far >= L ? s.n : min(s.n, far / KT + 1));
+    s.ng = s.nR > 0 ? g1 - g0 + 1 : 0;
+    // ... and local pairs if its largest position is at least L - w0 + 1
+    if (s.w0 == 0) {
+        s.kE0 = s.n;
+    } else {
+        const int lo = L - s.w0 + 1;
+        s.kE0 = lo <= 0 ? 0 : min(lo / KT, s.n);
+    }
+    s.items = s.ng * s.nR + (s.n - s.kE0);
+    s.row_tiles = (T * p.group + RT - 1) / RT;
+    return s;
+}
+
+// Workspace header: [0] per, [1] total, [2 + b] first item of request b.
+__host__ __device__ inline size_t paged_header_bytes(int B) { return ((size_t)(B + 3) * 8 + 255) / 256 * 256; }
+
+// Whole-CTA: prefix of the requests' item counts; returns through shared memory
+// the piece [start, end) of this CTA, the request it starts in and that
+// request's first item.  CTA 0 leaves the prefix in the workspace header.
+struct PiecePlan {
+    long long start, end, base, total;
+    int b;
+};
+
+template <int KT, int RT, int NTHR>
+__device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out, long long* scratch /* [NTHR/32 + 1] */)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int each = (p.B + NTHR - 1) / NTHR;
+    const int b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const SeqPlan s = seq_plan<KT, RT>(p, b, blockIdx.x == 0);
+        mine += (long long)s.items * s.row_tiles * p.Hkv;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < NTHR / 32; ++w) {
+        const long long x = scratch[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    long long at = before + incl - mine;  // first item of this thread's requests
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < min_items) per = min_items;
+    const long long start = min(total, per * blockIdx.x), end = min(total, start + per);
+    if (tid == 0) {
+        out->start = start;
+        out->end = end;
+        out->total = total;
+    }
+    const bool owner = start < end && at <= start && start < at + mine;
+    if (owner || blockIdx.x == 0) {
+        long long* head = reinterpret_cast<long long*>(p.workspace);
+        if (blockIdx.x == 0 && tid == 0) {
+            head[0] = per;
+            head[1] = total;
+            head[2 + p.B] = total;
+        }
+        for (int b = b0; b < b1; ++b) {
+            const SeqPlan s = seq_plan<KT, RT>(p, b, false);
+            const long long c = (long long)s.items * s.row_tiles * p.Hkv;
+            if (blockIdx.x == 0) head[2 + b] = at;
+            if (owner && at <= start && start < at + c) {
+                out->b = b;
+                out->base = at;
+            }
+            at += c;
+        }
+    }
+    __syncthreads();
+}
+
+// One item of a unit: the group size its keys are aliased by (0: exact
+// positions) and its key tile.
+__device__ __forceinline__ void item_of(const SeqPlan& s, int i, int* g, int* tile)
+{
+    const int rem = s.ng * s.nR;
+    if (i < rem) {
+        *g = s.gmin + i / s.nR;
+        *tile = i % s.nR;
+    } else {
+        *g = 0;
+        *tile = s.kE0 + (i - rem);
+    }
+}
+
+// Depth and ancestors-or-self of the T nodes of a request, by threads
+// 0 .. kMaxNodes - 1; par is shared scratch.  A parent that does not precede
+// its node counts as -1.
+__device__ inline void load_tree(const PagedProblem& p, const SeqPlan& s, int* par, int* depth, unsigned long long* anc)
+{
+    const int t = threadIdx.x;
+    if (t < s.T) {
+        int x = t - 1;
+        if (p.parents) {
+            x = p.parents[s.n0 + t];
+            if (x < -1 || x >= t) {
+                record_input(p.input_error, kBadParent);
+                x = -1;
+            }
+        }
+        par[t] = x;
+    }
+    __syncthreads();
+    if (t < s.T) {
+        unsigned long long m = 0;
+        if (p.parents) {
+            for (int x = t; x >= 0; x = par[x]) m |= 1ull << x;
+        } else {
+            m = (2ull << t) - 1;  // t = 63: 2 << 63 is 0, so all ones
+        }
+        anc[t] = m;
+        depth[t] = __popcll(m) - 1;
+    }
+    __syncthreads();
+}
+
+#endif  // __CUDACC__
+
+}  // namespace jl
