@@ -364,26 +364,49 @@ cudaError_t run_simt(const PagedProblem& p, cudaStream_t st, int* nlaunch)
     return e;
 }
 
-template <typename T, int D>
-cudaError_t run_dtype(const PagedProblem& p, cudaStream_t st, int* nlaunch)
+template <int D>
+cudaError_t run_fp32(const PagedProblem& p, cudaStream_t st, int* nlaunch)
 {
-    if (p.max_nodes * p.group <= 8) return run_simt<T, D, 8>(p, st, nlaunch);
-    return run_simt<T, D, 16>(p, st, nlaunch);
+    if (p.max_nodes * p.group <= 8) return run_simt<float, D, 8>(p, st, nlaunch);
+    return run_simt<float, D, 16>(p, st, nlaunch);
+}
+
+template <int D, int NCOL>
+cudaError_t merge_tc(const PagedProblem& p, cudaStream_t st)
+{
+    const int row_tiles = (p.max_nodes * p.group + NCOL - 1) / NCOL;
+    return launch_after(decode_paged_merge_kernel<__nv_bfloat16, D, 128, NCOL>, dim3(row_tiles, p.Hkv, p.B), D, st, p);
+}
+
+template <int D>
+cudaError_t run_bf16(const PagedProblem& p, cudaStream_t st, int* nlaunch)
+{
+    cudaError_t e = launch_decode_paged_tc(p, D, st);
+    if (e != cudaSuccess) return e;
+    *nlaunch += 1;
+    switch (paged_tc_columns(p.max_nodes * p.group)) {
+        case 16: e = merge_tc<D, 16>(p, st); break;
+        case 32: e = merge_tc<D, 32>(p, st); break;
+        case 64: e = merge_tc<D, 64>(p, st); break;
+        default: e = merge_tc<D, 128>(p, st); break;
+    }
+    if (e == cudaSuccess) *nlaunch += 1;
+    return e;
 }
 
 }  // namespace
 
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_nodes)
 {
-    (void)Hq; (void)Hkv; (void)max_nodes;
-    return paged_header_bytes(B) + (size_t)kSimtCtas * 2 * 16 * (d + 2) * sizeof(float);
+    const int rows = max_nodes * (Hq / Hkv);
+    const size_t simt = (size_t)kSimtCtas * 2 * (rows <= 8 ? 8 : 16) * (d + 2) * sizeof(float);
+    return paged_header_bytes(B) + std::max(simt, paged_tc_workspace(rows, d));
 }
 
 cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch)
 {
-    if (dt == JETLONG_FP32)
-        return d == 64 ? run_dtype<float, 64>(p, s, nlaunch) : run_dtype<float, 128>(p, s, nlaunch);
-    return d == 64 ? run_dtype<__nv_bfloat16, 64>(p, s, nlaunch) : run_dtype<__nv_bfloat16, 128>(p, s, nlaunch);
+    if (dt == JETLONG_FP32) return d == 64 ? run_fp32<64>(p, s, nlaunch) : run_fp32<128>(p, s, nlaunch);
+    return d == 64 ? run_bf16<64>(p, s, nlaunch) : run_bf16<128>(p, s, nlaunch);
 }
 
 }  // namespace jl

@@ -953,6 +953,7 @@ int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, v
     jl::PagedProblem p{};
     st = check_pages(num_pages, page_size, max_pages, &p.page_shift);
     if (st != JETLONG_OK) return st;
+    if ((int64_t)num_pages * Hkv > 2147483647LL) return fail(JETLONG_ERR_UNSUPPORTED, "num_pages * Hkv must fit 31 bits");
     const size_t need = jl::paged_workspace_bytes(B, Hq, Hkv, d, max_nodes);
     if (workspace_bytes < need)
         return fail(JETLONG_ERR_INVALID_ARG, "workspace too small (%zu < %zu bytes)", workspace_bytes, need);
@@ -970,6 +971,7 @@ int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, v
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     jl::make_rope_turns(&p.turns, d, rope_theta);
     p.workspace = static_cast<unsigned char*>(workspace);
+    take_injection(&p.inject, &p.wait_cycles);
     int n = 0;
     e = jl::launch_decode_paged(p, d, dtype, (cudaStream_t)stream, &n);
     g_launches += n;
