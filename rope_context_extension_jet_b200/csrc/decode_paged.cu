@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     piece_plan<PS_KT, RT, PS_NT>(p, 2, plan, reinterpret_cast<long long*>(plan + 1));
+    if (tid == 0) clear_cut(p);
     long long cur = plan->start, base = plan->base;
     const long long end = plan->end;
     int b = plan->b;
@@ -93,7 +94,8 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
             s = seq_plan<PS_KT, RT>(p, b, false);
             cnt = (long long)s.items * s.row_tiles * p.Hkv;
         }
-        const int unit = (int)((cur - base) / s.items), i0 = (int)((cur - base) % s.items);
+        int unit, i0;
+        div_items(cur - base, s.items, &unit, &i0);
         const int i1 = (int)min((long long)s.items, i0 + (end - cur));
         const int kvh = unit / s.row_tiles, rt = unit % s.row_tiles;
         const int r0 = rt * RT, nrows = min(RT, s.T * p.group - r0);
@@ -113,9 +115,10 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
 #pragma unroll
         for (int r = 0; r < RT; ++r) o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
         int gcur = -1;
-        for (int it = i0; it < i1; ++it) {
-            int g, tile;
-            item_of(s, it, &g, &tile);
+        Items item;
+        item.start(s, i0);
+        for (int it = i0; it < i1; ++it, item.next(s)) {
+            const int g = item.g, tile = item.tile;
             __syncthreads();  // the previous tile is used up; qpos is ready
             if (g != gcur) {
                 gcur = g;
@@ -263,7 +266,8 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
         }
         // sum the key slices through shared memory, eight rows at a time, and write
         const bool whole = i0 == 0 && i1 == s.items;
-        float* part = reinterpret_cast<float*>(p.workspace + paged_header_bytes(p.B)) +
+        if (tid == 0 && i0 == 0 && !whole) note_cut(p, s, plan->per, cur, kvh, r0, nrows);
+        float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
                       ((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * RT * (D + 2);
         float* red = kr;  // [KS][8][D] = PS_NT * 32 floats: fits kr and vs together
 #pragma unroll
@@ -294,39 +298,93 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
     }
 }
 
+constexpr int MG_NT = 256, MG_SPLIT = 4, MG_ROWS = MG_NT / 32 / MG_SPLIT;
+
 // Joins the pieces of every unit that was cut: out = sum_c 2^(m_c - M) o_c /
-// sum_c 2^(m_c - M) l_c, pieces in ascending order, so results do not depend on
-// which CTA finished first.  One CTA per possible unit; units that lie in one
-// piece were written already.
-template <typename T, int D, int KT, int RT>
-__global__ void __launch_bounds__(D) decode_paged_merge_kernel(PagedProblem p)
+// sum_c 2^(m_c - M) l_c.  blockIdx.x is the CTA whose piece begins the unit (at
+// most one such unit per CTA), blockIdx.y a pair of its rows; four warps share a
+// row, each summing every fourth run of pieces in ascending order, so the result
+// does not depend on which CTA finished first.
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(MG_NT) decode_paged_merge_kernel(PagedProblem p)
 {
+    constexpr int V = D / 32;  // columns per lane
+    __shared__ float s_o[MG_NT / 32][D];
+    __shared__ float s_m[MG_NT / 32], s_l[MG_NT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long* head = reinterpret_cast<const long long*>(p.workspace);
-    const int b = blockIdx.z, kvh = blockIdx.y, rt = blockIdx.x;
-    const SeqPlan s = seq_plan<KT, RT>(p, b, false);
-    if (rt >= s.row_tiles) return;
-    const long long per = __ldcg(head);
-    const long long first = __ldcg(head + 2 + b) + ((long long)kvh * s.row_tiles + rt) * s.items, last = first + s.items - 1;
-    const long long c0 = first / per, c1 = last / per;
-    if (c0 == c1) return;
-    const float* parts = reinterpret_cast<const float*>(p.workspace + paged_header_bytes(p.B));
-    const int r0 = rt * RT, nrows = min(RT, s.T * p.group - r0), c = threadIdx.x;
-    for (int r = 0; r < nrows; ++r) {
-        float M = -INFINITY, num = 0.f, den = 0.f;
-        for (long long x = c0; x <= c1; ++x) {
-            const float* row = parts + ((size_t)(x * 2 + (x == c0 ? 1 : 0)) * RT + r) * (D + 2);
-            const float m = __ldcg(row + D), l = __ldcg(row + D + 1), v = __ldcg(row + c);
-            const float mn = fmaxf(M, m), ref = mn == -INFINITY ? 0.f : mn;
-            const float wa = exp2f(M - ref), wb = exp2f(m - ref);
-            num = num * wa + v * wb;
-            den = den * wa + l * wb;
+    const CutUnit* cut = reinterpret_cast<const CutUnit*>(p.workspace) + blockIdx.x;
+    const int rows = __ldcg(&cut->rows), pieces = __ldcg(&cut->pieces);
+    if ((int)blockIdx.y * MG_ROWS >= rows) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.y * MG_ROWS + warp / MG_SPLIT, sub = warp % MG_SPLIT;
+    const float* parts = reinterpret_cast<const float*>(p.workspace + kPagedHeader);
+    float M = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) o[u] = 0.f;
+    // piece x: slot 2 c + 1 of the CTA that begins the unit, slot 2 (c + x) of the others
+    auto piece = [&](int x) { return parts + ((size_t)(2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)) * RT + r) * (D + 2); };
+    if (r < rows) {
+        const int each = (pieces + MG_SPLIT - 1) / MG_SPLIT, x1 = min(pieces, (sub + 1) * each);
+        for (int x0 = sub * each; x0 < x1; x0 += 32) {
+            // lane x holds the maximum and sum of piece x0 + x
+            const int cnt = min(32, x1 - x0);
+            float m = -INFINITY, ls = 0.f;
+            if (lane < cnt) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(piece(x0 + lane) + D));
+                m = ml.x;
+                ls = ml.y;
+            }
+            float mx = m;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float mn = fmaxf(M, mx), ref = mn == -INFINITY ? 0.f : mn;
+            const float a = exp2f(M - ref), wgt = exp2f(m - ref);
             M = mn;
+            float add = wgt * ls;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) add += __shfl_xor_sync(0xffffffffu, add, w);
+            l = l * a + add;
+#pragma unroll
+            for (int u = 0; u < V; ++u) o[u] *= a;
+#pragma unroll 8
+            for (int x = 0; x < cnt; ++x) {
+                const float wx = __shfl_sync(0xffffffffu, wgt, x);
+                const float* row = piece(x0 + x) + lane * V;
+                if (wx != 0.f) {  // a piece without a key of this row holds no values
+#pragma unroll
+                    for (int u = 0; u < V; u += 2) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2*>(row + u));
+                        o[u] = fmaf(wx, v.x, o[u]);
+                        o[u + 1] = fmaf(wx, v.y, o[u + 1]);
+                    }
+                }
+            }
         }
-        const int node = (r0 + r) / p.group, hd = kvh * p.group + (r0 + r) % p.group;
-        store_elem(static_cast<T*>(p.out) + ((size_t)(s.n0 + node) * p.Hq + hd) * D + c, num / den);
+#pragma unroll
+        for (int u = 0; u < V; ++u) s_o[warp][lane * V + u] = o[u];
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_l[warp] = l;
+        }
     }
+    __syncthreads();
+    const int rr = threadIdx.x / (MG_NT / MG_ROWS), c = threadIdx.x % (MG_NT / MG_ROWS), row = blockIdx.y * MG_ROWS + rr;
+    if (row >= rows || c >= D) return;
+    float M4 = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll
+    for (int x = 0; x < MG_SPLIT; ++x) M4 = fmaxf(M4, s_m[rr * MG_SPLIT + x]);
+    const float ref = M4 == -INFINITY ? 0.f : M4;
+#pragma unroll
+    for (int x = 0; x < MG_SPLIT; ++x) {
+        const float w = exp2f(s_m[rr * MG_SPLIT + x] - ref);
+        num = fmaf(w, s_o[rr * MG_SPLIT + x][c], num);
+        den = fmaf(w, s_l[rr * MG_SPLIT + x], den);
+    }
+    const int r_unit = cut->r0 + row, node = cut->node0 + r_unit / p.group, hd = cut->head0 + r_unit % p.group;
+    store_elem(static_cast<T*>(p.out) + ((size_t)node * p.Hq + hd) * D + c, num / den);
 }
+
+int merge_rows(const PagedProblem& p, int rt) { return (std::min(rt, p.max_nodes * p.group) + MG_ROWS - 1) / MG_ROWS; }
 
 // Starts while the attention kernel runs and waits for its end on the device.
 template <class Kern>
@@ -358,8 +416,7 @@ cudaError_t run_simt(const PagedProblem& p, cudaStream_t st, int* nlaunch)
     decode_paged_simt_kernel<T, D, RT><<<grid, PS_NT, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *nlaunch += 1;
-    const int row_tiles = (p.max_nodes * p.group + RT - 1) / RT;
-    e = launch_after(decode_paged_merge_kernel<T, D, PS_KT, RT>, dim3(row_tiles, p.Hkv, p.B), D, st, p);
+    e = launch_after(decode_paged_merge_kernel<T, D, RT>, dim3(grid, merge_rows(p, RT)), MG_NT, st, p);
     if (e == cudaSuccess) *nlaunch += 1;
     return e;
 }
@@ -372,23 +429,23 @@ cudaError_t run_fp32(const PagedProblem& p, cudaStream_t st, int* nlaunch)
 }
 
 template <int D, int NCOL>
-cudaError_t merge_tc(const PagedProblem& p, cudaStream_t st)
+cudaError_t merge_tc(const PagedProblem& p, int grid, cudaStream_t st)
 {
-    const int row_tiles = (p.max_nodes * p.group + NCOL - 1) / NCOL;
-    return launch_after(decode_paged_merge_kernel<__nv_bfloat16, D, 128, NCOL>, dim3(row_tiles, p.Hkv, p.B), D, st, p);
+    return launch_after(decode_paged_merge_kernel<__nv_bfloat16, D, NCOL>, dim3(grid, merge_rows(p, NCOL)), MG_NT, st, p);
 }
 
 template <int D>
 cudaError_t run_bf16(const PagedProblem& p, cudaStream_t st, int* nlaunch)
 {
-    cudaError_t e = launch_decode_paged_tc(p, D, st);
+    int grid = 0;
+    cudaError_t e = launch_decode_paged_tc(p, D, st, &grid);
     if (e != cudaSuccess) return e;
     *nlaunch += 1;
     switch (paged_tc_columns(p.max_nodes * p.group)) {
-        case 16: e = merge_tc<D, 16>(p, st); break;
-        case 32: e = merge_tc<D, 32>(p, st); break;
-        case 64: e = merge_tc<D, 64>(p, st); break;
-        default: e = merge_tc<D, 128>(p, st); break;
+        case 16: e = merge_tc<D, 16>(p, grid, st); break;
+        case 32: e = merge_tc<D, 32>(p, grid, st); break;
+        case 64: e = merge_tc<D, 64>(p, grid, st); break;
+        default: e = merge_tc<D, 128>(p, grid, st); break;
     }
     if (e == cudaSuccess) *nlaunch += 1;
     return e;
@@ -400,7 +457,7 @@ size_t paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_nodes)
 {
     const int rows = max_nodes * (Hq / Hkv);
     const size_t simt = (size_t)kSimtCtas * 2 * (rows <= 8 ? 8 : 16) * (d + 2) * sizeof(float);
-    return paged_header_bytes(B) + std::max(simt, paged_tc_workspace(rows, d));
+    return kPagedHeader + std::max(simt, paged_tc_workspace(rows, d));
 }
 
 cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch)

@@ -74,7 +74,7 @@ cudaError_t launch_tree_commit(const CommitProblem& p, cudaStream_t s, int* nlau
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_nodes);
 int paged_tc_columns(int rows);
 size_t paged_tc_workspace(int rows, int d);
-cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s);
+cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s, int* grid);
 cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch);
 
 __device__ __forceinline__ void record_input(int* word, int code)
@@ -112,6 +112,19 @@ struct SeqPlan {
     int row_tiles;
 };
 
+// Largest depth of a tree (a parent that does not precede its node counts as -1).
+__device__ inline int tree_depth(const int* parents, int T)
+{
+    unsigned char d[kMaxNodes];
+    int most = 0;
+    for (int t = 0; t < T; ++t) {
+        const int x = parents[t];
+        d[t] = (unsigned char)(x >= 0 && x < t ? d[x] + 1 : 0);
+        most = max(most, (int)d[t]);
+    }
+    return most;
+}
+
 template <int KT, int RT>
 __device__ inline SeqPlan seq_plan(const PagedProblem& p, int b, bool report)
 {
@@ -142,8 +155,14 @@ __device__ inline SeqPlan seq_plan(const PagedProblem& p, int b, bool report)
         s.w0 = 0;
         return s;
     }
-    const int imax = L + T - 1;  // no node is deeper than T - 1
-    const int g0 = L / p.w_pre + 1, g1 = imax / p.w_pre + 1;
+    const int g0 = L / p.w_pre + 1;
+    int imax = L + T - 1;  // no node is deeper than T - 1
+    int g1 = imax / p.w_pre + 1;
+    if (g1 > g0 && p.parents) {
+        // a chain would cross into the next group size: the tree may not
+        imax = L + tree_depth(p.parents + a, T);
+        g1 = imax / p.w_pre + 1;
+    }
     s.n = (L + T + KT - 1) / KT;
     s.gmin = g0;
     s.w0 = p.w0;
@@ -165,19 +184,26 @@ __device__ inline SeqPlan seq_plan(const PagedProblem& p, int b, bool report)
     return s;
 }
 
-// Workspace header: [0] per, [1] total, [2 + b] first item of request b.
-__host__ __device__ inline size_t paged_header_bytes(int B) { return ((size_t)(B + 3) * 8 + 255) / 256 * 256; }
+// Workspace: one CutUnit per CTA (the unit its piece begins and does not end, if
+// any), then two partial states per CTA.
+struct CutUnit {
+    int rows;        // 0: none
+    int pieces;      // CTAs c, c + 1, ... c + pieces - 1 hold it
+    int node0, head0, r0;  // token row of the request's first node, first query head, first row of the unit
+    int pad[3];
+};
+constexpr size_t kPagedHeader = 512 * sizeof(CutUnit);
 
-// Whole-CTA: prefix of the requests' item counts; returns through shared memory
-// the piece [start, end) of this CTA, the request it starts in and that
-// request's first item.  CTA 0 leaves the prefix in the workspace header.
+// Whole-CTA: running sum of the requests' item counts; returns through shared
+// memory the piece [start, end) of this CTA, the request it starts in and that
+// request's first item.
 struct PiecePlan {
-    long long start, end, base, total;
+    long long start, end, base, per;
     int b;
 };
 
 template <int KT, int RT, int NTHR>
-__device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out, long long* scratch /* [NTHR/32 + 1] */)
+__device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out, long long* scratch /* [NTHR/32] */)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int each = (p.B + NTHR - 1) / NTHR;
@@ -208,21 +234,13 @@ __device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out,
     if (tid == 0) {
         out->start = start;
         out->end = end;
-        out->total = total;
+        out->per = per;
     }
-    const bool owner = start < end && at <= start && start < at + mine;
-    if (owner || blockIdx.x == 0) {
-        long long* head = reinterpret_cast<long long*>(p.workspace);
-        if (blockIdx.x == 0 && tid == 0) {
-            head[0] = per;
-            head[1] = total;
-            head[2 + p.B] = total;
-        }
+    if (start < end && at <= start && start < at + mine) {
         for (int b = b0; b < b1; ++b) {
             const SeqPlan s = seq_plan<KT, RT>(p, b, false);
             const long long c = (long long)s.items * s.row_tiles * p.Hkv;
-            if (blockIdx.x == 0) head[2 + b] = at;
-            if (owner && at <= start && start < at + c) {
+            if (at <= start && start < at + c) {
                 out->b = b;
                 out->base = at;
             }
@@ -232,17 +250,59 @@ __device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out,
     __syncthreads();
 }
 
-// One item of a unit: the group size its keys are aliased by (0: exact
-// positions) and its key tile.
-__device__ __forceinline__ void item_of(const SeqPlan& s, int i, int* g, int* tile)
+// Record of the unit this CTA's piece begins and does not end.  One thread per CTA
+// writes it before the walk ends; a CTA that cuts no unit so leaves rows = 0.
+__device__ __forceinline__ void clear_cut(const PagedProblem& p)
 {
-    const int rem = s.ng * s.nR;
-    if (i < rem) {
-        *g = s.gmin + i / s.nR;
-        *tile = i % s.nR;
+    reinterpret_cast<CutUnit*>(p.workspace)[blockIdx.x].rows = 0;
+}
+__device__ __forceinline__ void note_cut(const PagedProblem& p, const SeqPlan& s, long long per, long long first, int kvh,
+                                         int r0, int rows)
+{
+    CutUnit* c = reinterpret_cast<CutUnit*>(p.workspace) + blockIdx.x;
+    c->rows = rows;
+    c->pieces = (int)((first + s.items - 1) / per - first / per + 1);
+    c->node0 = s.n0;
+    c->head0 = kvh * p.group;
+    c->r0 = r0;
+}
+
+// The items of a unit in order: the group size its keys are aliased by (0: exact
+// positions) and the key tile.
+struct Items {
+    int g, tile;
+    __device__ __forceinline__ void start(const SeqPlan& s, int i)
+    {
+        const int rem = s.ng * s.nR;
+        if (i < rem) {
+            g = s.gmin + i / s.nR;
+            tile = i % s.nR;
+        } else {
+            g = 0;
+            tile = s.kE0 + (i - rem);
+        }
+    }
+    __device__ __forceinline__ void next(const SeqPlan& s)
+    {
+        ++tile;
+        if (g != 0 && tile == s.nR) {
+            const bool more = g + 1 < s.gmin + s.ng;
+            tile = more ? 0 : s.kE0;
+            g = more ? g + 1 : 0;
+        }
+    }
+};
+
+// Quotient and remainder of a unit's place by its items; 64-bit division only
+// where it is needed.
+__device__ __forceinline__ void div_items(long long x, int items, int* q, int* r)
+{
+    if (x <= 0xffffffffll) {
+        *q = (int)((unsigned)x / (unsigned)items);
+        *r = (int)((unsigned)x % (unsigned)items);
     } else {
-        *g = 0;
-        *tile = s.kE0 + (i - rem);
+        *q = (int)(x / items);
+        *r = (int)(x % items);
     }
 }
 
