@@ -441,11 +441,11 @@ cudaError_t run_bf16(const PagedProblem& p, cudaStream_t st, int* nlaunch)
     cudaError_t e = launch_decode_paged_tc(p, D, st, &grid);
     if (e != cudaSuccess) return e;
     *nlaunch += 1;
-    switch (paged_tc_columns(p.max_nodes * p.group)) {
+    switch (paged_tc_rows(p.max_nodes * p.group)) {
         case 16: e = merge_tc<D, 16>(p, grid, st); break;
         case 32: e = merge_tc<D, 32>(p, grid, st); break;
-        case 64: e = merge_tc<D, 64>(p, grid, st); break;
-        default: e = merge_tc<D, 128>(p, grid, st); break;
+        case 128: e = merge_tc<D, 128>(p, grid, st); break;
+        default: e = merge_tc<D, 256>(p, grid, st); break;
     }
     if (e == cudaSuccess) *nlaunch += 1;
     return e;

@@ -1,0 +1,459 @@
+// decode_paged_rows.cu -- bf16 decode over a paged raw-key cache for more than 32
+// query rows per request and kv head (larger drafted trees, wide head groups), with
+// the query rows as the 128 rows of the products (mathematics and work plan:
+// decode_paged.cu, paged_common.cuh; shared roles: paged_tc_roles.cuh).
+//
+//   S [128 rows x 128 keys] = Q_rot [128 x d] K_rot^T      (fp16 operands)
+//   O [128 rows x d]       += P [128 x 128] V              (bf16 operands, P in TMEM)
+// A softmax thread owns one row (one TMEM lane), so the running reference, the sum
+// and the rescale factor are its own and no element needs a per-column factor; from
+// about 32 rows on that beats the form of decode_paged_tc.cu, whose cost per key
+// grows with the rows.  Two softmax warpgroups ("streams") overlap: one computes
+// while the tensor cores work for the other.
+//   ROWS = 256: stream s holds rows [128 s, 128 s + 128); both use every key tile,
+//     which is loaded and rotated once for all 256.
+//   ROWS = 128: both hold the same rows and take the tiles in turn; each keeps its
+//     own reference, sum and O, joined where the unit ends.
+//
+// Warp roles: 0 / 3 producers, 1 MMA issuer, 2 tensor memory and planner, 4-7
+// rotation, 8-11 / 12-15 softmax of stream 0 / 1.
+// TMEM (512 columns): S_0, S_1 (128 each; P_s over the first 64 of S_s), O_0, O_1.
+#include <algorithm>
+
+#include "paged_tc_roles.cuh"
+
+namespace jl {
+namespace ptc {
+
+template <int D, int NROWS>
+struct RowTiles {
+    static constexpr int DIM = D, ROWS = NROWS;
+    static constexpr int NSK = D == 64 ? 4 : NROWS == 128 ? 3 : 2, NSV = D == 64 ? 4 : 2;
+    static constexpr int THREADS = 512;
+    static constexpr bool ALT = false;
+    static constexpr int ROT = 128, ROTALL = 128, SOFT = 8;
+    static constexpr int ATOMS = D / 64;
+    static constexpr int TILE = KT * D * 2, ATOM_K = KT * 128;
+    static constexpr int K0 = 0, V0 = K0 + NSK * TILE, Q0 = V0 + NSV * TILE, BASE = Q0 + NROWS * D * 2;
+    static __device__ __forceinline__ uint32_t q_off(int r, int ch) { return (r >> 7) * TILE + tc::sw128_off<128>(r & 127, ch); }
+};
+template <int D, int NROWS>
+struct RowCfg : RowTiles<D, NROWS>,
+                Notes<D, NROWS, RowTiles<D, NROWS>::NSK, RowTiles<D, NROWS>::NSV, RowTiles<D, NROWS>::BASE, 8, 16> {
+    static constexpr int XCH = RowCfg::NOTES_END;  // [2][128] (reference, sum) of the streams
+    static constexpr int TOTAL = XCH + 2 * 128 * 8 + 1024;
+    static_assert(TOTAL <= 232448, "shared memory");
+    // Registers per thread after setmaxnreg: producers / issuer / planner, rotation,
+    // each softmax warpgroup.  An increase draws on what the block was launched with
+    // (512 x 128).
+    static constexpr int R_PROD = 56, R_ROT = 96, R_SOFT = 176;
+    static_assert((R_PROD + R_ROT + 2 * R_SOFT) * 128 <= 512 * 128, "register split");
+};
+
+template <int D, int NROWS>
+__global__ void __launch_bounds__(512, 1)
+    decode_paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                             const __grid_constant__ PagedProblem p, const Launch ln)
+{
+    using C = RowCfg<D, NROWS>;
+    constexpr bool PAIR = NROWS == 256;
+    constexpr int NSK = C::NSK, NSV = C::NSV;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const Role<C> ro(p, ln, smem);
+    const Bars<C>& bars = ro.bars;
+    uint64_t *sfull = bars.extra, *pfull = sfull + 2, *pvdone = pfull + 4;  // per stream; pfull per half of the keys
+    const int warp = ro.warp, lane = ro.lane;
+    const uint32_t tmem = start_cta<C, 512>(ro, [&] {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sfull[s], 1);
+            mbar_init(&pfull[2 * s], 4);
+            mbar_init(&pfull[2 * s + 1], 4);
+            mbar_init(&pvdone[s], 1);
+        }
+    });
+    if (warp < 4) {
+        regs_dec<C::R_PROD>();
+        if (warp == 0) {
+            produce<C, true>(ro, &tmK);
+        } else if (warp == 3) {
+            produce<C, false>(ro, &tmV);
+        } else if (warp == 2) {
+            plan_units<C>(ro);
+        } else {
+            // -------------------------------------------------- MMA issuer
+            // A task is one item on one stream: S_s = Q K^T, later O_s += P_s V.  P_s
+            // lies over S_s, so a stream's P V is issued before its next Q K^T (one
+            // issuer's MMAs run in order).
+            constexpr uint32_t IQK = idesc_f16(128, KT, 0), IPV = idesc_bf16(128, D, 1);
+            const uint32_t sb = smem_u32(smem);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            int e = 0, phases = 0;
+            unsigned nfix = 0;              // per stage: parity of the repaired value tiles so far
+            int done[2] = {0, 0};           // P V of each stream so far
+            int pe[2] = {-1, -1};           // its pending item
+            bool pfirst[2] = {false, false}, pfix[2] = {false, false};
+            bool ok = true;
+            const unsigned all_pages = ro.all_pages();
+            auto pv = [&](int s) {
+                const int x = pe[s], st = x % NSV;
+                if (!ro.wait(&bars.vfull[st], (x / NSV) & 1, 0x512)) return false;
+                if (pfix[s] && !(PAIR && s == 1)) {  // both streams use the tile: stream 0 comes first
+                    if (!ro.wait(&bars.vfix[st], (nfix >> st) & 1, 0x513)) return false;
+                    nfix ^= 1u << st;
+                }
+                const uint64_t vd = sdesc_sw128(sb + C::V0 + st * C::TILE, C::ATOM_K, 1024);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!ro.wait(&pfull[2 * s + half], done[s] & 1, 0x511)) return false;
+                    tc_fence_after();
+                    umma_pv_k64(tm + 256 + s * 128, tm + s * 128 + 32 * half, vd + 512 * half, IPV, pfirst[s] && half == 0 ? 0u : 1u);
+                }
+                umma_commit_elect(&pvdone[s]);
+                if (!PAIR || s == 1) umma_commit_elect(&bars.vempty[st]);
+                ++done[s];
+                pe[s] = -1;
+                return true;
+            };
+            for (int k = 0; ok; ++k) {
+                if (!ro.unit_wait(k, 0x516)) break;
+                UnitPtr un = ro.unit(k);
+                if (un->rows == 0) break;
+                const int L = un->L;
+                int gcur = -1, li = 0;
+                for (UnitItems it(un); ok && it.left > 0; it.next(un), ++e, ++li) {
+                    const int st = e % NSK;
+                    bool fix = false;
+                    for (int s = PAIR ? 0 : li & 1, s1 = PAIR ? 1 : s; s <= s1; ++s) {
+                        if (pe[s] >= 0 && !pv(s)) { ok = false; break; }
+                        if (s == 0 || !PAIR) {
+                            if (it.g != gcur) {
+                                gcur = it.g;
+                                if (!ro.wait(bars.qready, phases & 1, 0x515)) { ok = false; break; }
+                                ++phases;
+                            }
+                            if (!ro.wait(&bars.kready[st], (e / NSK) & 1, 0x514)) { ok = false; break; }
+                            fix = (it.tile + 1) * KT > L || ro.note()[e % INFO] != all_pages;
+                        }
+                        tc_fence_after();
+                        const uint64_t a = sdesc_sw128(sb + C::Q0 + (PAIR ? s * C::TILE : 0), 16, 1024);
+                        const uint64_t b = sdesc_sw128(sb + C::K0 + st * C::TILE, 16, 1024);
+                        if (D == 128)
+                            umma_qk_k128(tm + s * 128, a, b, IQK);
+                        else
+                            umma_qk_k64(tm + s * 128, a, b, IQK);
+                        umma_commit_elect(&sfull[s]);
+                        if (!PAIR || s == 1) umma_commit_elect(&bars.kempty[st]);
+                        pe[s] = e;
+                        pfirst[s] = PAIR ? li == 0 : li < 2;
+                        pfix[s] = fix;
+                    }
+                }
+                for (int s = 0; s < 2 && ok; ++s)
+                    if (pe[s] >= 0 && !pv(s)) ok = false;
+                ro.unit_done(k);
+            }
+            umma_commit_elect(bars.drain);
+            mbar_wait(bars.drain, 0);
+        }
+    } else if (warp < 8) {
+        regs_dec<C::R_ROT>();
+        rotate_keys<C>(ro);
+    } else {
+        regs_inc<C::R_SOFT>();
+        // ------------------------------------------------------ softmax
+        constexpr int bid = 2;  // named barrier of both warpgroups
+        const int s = (warp - 8) >> 2, lrow = (warp & 3) * 32 + lane, row = (PAIR ? s * 128 : 0) + lrow;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_col = lanes + s * 128, o_col = lanes + 256 + s * 128;
+        const float* ksc = reinterpret_cast<const float*>(smem + C::KSC);
+        float2* xch = reinterpret_cast<float2*>(smem + C::XCH);
+        const int gshift = min(p.page_shift, 7);
+        const unsigned all_pages = ro.all_pages();
+        int e = 0, nu = 0, done = 0;  // items, units, tasks of this stream
+        // a wait that ran out is carried to the next barrier of the two warpgroups,
+        // where their eight warps stop together
+        bool ok = true;
+        for (;; ++nu) {
+            ok = ro.unit_wait(nu, 0x536);
+            UnitPtr ud = ro.unit(nu);
+            if (ok && ud->rows == 0) {
+                named_or(bid, 256, false);  // meets a warp that gave up waiting for the unit
+                break;
+            }
+            const unsigned char* un = smem + C::UNIT + (nu & 1) * C::UBYTES;
+            const int* depth = reinterpret_cast<const int*>(un + C::U_DEPTH);
+            ok = ok && ro.wait(&bars.uready[nu & 1], (nu >> 1) & 1, 0x531);
+            const int lim = reinterpret_cast<const int*>(un + C::U_LIM)[row], G = reinterpret_cast<const int*>(un + C::U_QG)[row];
+            const float cq = reinterpret_cast<const float*>(un + C::U_CQ)[row];
+            const unsigned long long anc = reinterpret_cast<const unsigned long long*>(un + C::U_ANC)[row];
+            float ref = kNoRef, l = 0.f;
+            unsigned long long nodes = 0;  // drafted nodes this row attends in the current phase
+            int gcur = -1, li = 0, mine = 0;
+            if (ok) {
+                for (UnitItems it(ud); it.left > 0; it.next(ud), ++e, ++li) {
+                    if (!PAIR && (li & 1) != s) continue;
+                    const int g = it.g, j0 = it.tile * KT, L = ud->L, T = ud->T;
+                    if (!ro.wait(&sfull[s], done & 1, 0x532)) { ok = false; break; }
+                    tc_fence_after();
+                    float x[KT];
+                    {
+                        uint32_t t0[32], t1[32], t2[32], t3[32];  // four loads in flight, one wait
+                        tmem_ld32(s_col, t0);
+                        tmem_ld32(s_col + 32, t1);
+                        tmem_ld32(s_col + 64, t2);
+                        tmem_ld32(s_col + 96, t3);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) {
+                            x[u] = __uint_as_float(t0[u]);
+                            x[32 + u] = __uint_as_float(t1[u]);
+                            x[64 + u] = __uint_as_float(t2[u]);
+                            x[96 + u] = __uint_as_float(t3[u]);
+                        }
+                    }
+                    const unsigned have = ro.note()[e % INFO];
+                    const volatile unsigned* sc4 = reinterpret_cast<const volatile unsigned*>(smem + C::SCALED) + (e % INFO) * 4;
+                    if ((sc4[0] | sc4[1]) | (sc4[2] | sc4[3])) {
+                        // some key rows were scaled by a power of two (paged_tc_roles.cuh)
+                        asm volatile("" ::: "memory");
+                        const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT);
+#pragma unroll
+                        for (int u = 0; u < KT; u += 4) {
+                            const float4 f = k4[u / 4];
+                            x[u] *= f.x;
+                            x[u + 1] *= f.y;
+                            x[u + 2] *= f.z;
+                            x[u + 3] *= f.w;
+                        }
+                    }
+                    const bool drafted = j0 + KT > L || have != all_pages;
+                    if (drafted || (g == 0 ? L + T - 1 - j0 >= ud->w0 : (ud->ng > 1 || L - (j0 + KT - 1) < ud->w0))) {
+                        asm volatile("" ::: "memory");  // a branch, not predication: most tiles skip this
+                        if (g != gcur) {
+                            gcur = g;
+                            nodes = 0;
+#pragma unroll 1
+                            for (int v = 0; v < T; ++v) {
+                                const bool local = L + depth[v] > lim;
+                                const bool keep = g == 0 ? local : (!local && G == g);
+                                nodes |= (unsigned long long)(keep && ((anc >> v) & 1)) << v;
+                            }
+                        }
+                        // committed keys: those past the border (exact phase) or up to it
+                        // (remote phase of this row's group size), before row L
+                        const int cut = lim < j0 ? 0 : lim - j0 + 1;  // keys [0, cut) of the tile are remote
+                        const int c0 = L - j0;         // keys [0, c0) are committed
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            auto below = [&](int n) {  // bits of this word's keys that lie in [0, n) of the tile
+                                const int m = n - 32 * w;
+                                return m <= 0 ? 0u : m >= 32 ? 0xffffffffu : (1u << m) - 1;
+                            };
+                            uint32_t bits = below(cut);
+                            bits = g == 0 ? ~bits : (G == g ? bits : 0u);
+                            bits &= below(c0);
+                            // node v is key c0 + v
+                            const int sh = 32 * w - c0;
+                            if (sh >= 0)
+                                bits |= sh < 64 ? (uint32_t)(nodes >> sh) : 0u;
+                            else if (sh > -32)
+                                bits |= (uint32_t)nodes << -sh;
+                            if (have != all_pages) {
+                                uint32_t there = 0;
+#pragma unroll 1
+                                for (int u = 0; u < 32; ++u) there |= ((have >> ((32 * w + u) >> gshift)) & 1u) << u;
+                                bits &= there;
+                            }
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) x[32 * w + u] = (bits >> u) & 1 ? x[32 * w + u] : -INFINITY;
+                        }
+                    }
+                    float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int u = 4; u < KT; u += 8) {
+                        m4[0] = fmax3(m4[0], x[u], x[u + 1]);
+                        m4[1] = fmax3(m4[1], x[u + 2], x[u + 3]);
+                        if (u + 4 < KT) {
+                            m4[2] = fmax3(m4[2], x[u + 4], x[u + 5]);
+                            m4[3] = fmax3(m4[3], x[u + 6], x[u + 7]);
+                        }
+                    }
+                    // logits in log2 units: x cq, cq > 0 a power of two times the scale
+                    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cq;
+                    float alpha = 1.f;
+                    const bool resc = mt > ref + kExceed;
+                    if (resc) {
+                        alpha = ex2_approx(ref - (mt + kAbove));
+                        ref = mt + kAbove;
+                        l *= alpha;
+                    }
+                    const float2 sl = make_float2(cq, cq), nm = make_float2(-ref, -ref);
+                    float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t pk[KT / 4];
+#pragma unroll
+                        for (int v = 0; v < KT / 2; v += 4) {
+                            const int u = half * (KT / 2) + v;
+                            const float2 y0 = fma2(make_float2(x[u], x[u + 1]), sl, nm);
+                            const float2 y1 = fma2(make_float2(x[u + 2], x[u + 3]), sl, nm);
+                            const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
+                            const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+                            acc0 = add2(acc0, p0);
+                            acc1 = add2(acc1, p1);
+                            pk[v >> 1] = pack_bf16x2(p0.x, p0.y);
+                            pk[(v >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
+                        }
+                        // the stream's last P V finished before this tile's Q K^T (issued
+                        // later by the same issuer); O is rescaled before any of this tile's P
+                        // is published
+                        if (half == 0 && mine > 0 && __any_sync(0xffffffffu, resc)) {
+                            if (!ro.wait(&pvdone[s], (done - 1) & 1, 0x533)) { ok = false; break; }
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int cc = 0; cc < D; cc += 16) {
+                                uint32_t tt[16];
+                                tmem_ld16(o_col + cc, tt);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) tt[u] = __float_as_uint(__uint_as_float(tt[u]) * alpha);
+                                tmem_st16(o_col + cc, tt);
+                            }
+                        }
+                        tmem_st32(s_col + half * 32, pk);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pfull[2 * s + half]);
+                    }
+                    if (!ok) break;
+                    l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                    ++done;
+                    ++mine;
+                }
+            }
+            // ---- the unit's piece is complete
+            if (ok && mine > 0) ok = ro.wait(&pvdone[s], (done - 1) & 1, 0x535);
+            if (!PAIR) xch[s * 128 + lrow] = make_float2(ref, l);
+            tc_fence_before();
+            if (named_or(bid, 256, !ok)) break;
+            tc_fence_after();
+            const int i0 = ud->i0, r0 = ud->r0, kvh = ud->kvh, rows = ud->rows;
+            const bool whole = i0 == 0 && ud->i1 == ud->items, live = row < rows;
+            float w0 = 1.f, w1 = 0.f;  // weights of this and the other stream's O
+            if (!PAIR) {
+                const float2 o = xch[(s ^ 1) * 128 + lrow];
+                const float top = fmaxf(ref, o.x);
+                w0 = ref == kNoRef ? 0.f : ex2_approx(ref - top);
+                w1 = o.x == kNoRef ? 0.f : ex2_approx(o.x - top);
+                l = w0 * l + w1 * o.y;
+                ref = top;
+            }
+            const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(un + C::U_BAD) & anc;
+            const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
+            float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
+                          (((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NROWS + row) * (D + 2);
+            __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + ((size_t)(ud->n0 + node) * p.Hq + hd) * D;
+            const float inv = 1.f / l;
+            // the streams of one row share its columns
+            const int cb0 = PAIR ? 0 : s * (D / 2), cb1 = PAIR ? D : cb0 + D / 2;
+#pragma unroll 1
+            for (int cb = cb0; cb < cb1; cb += 16) {
+                uint32_t a[16], b[16];
+                tmem_ld16(o_col + cb, a);
+                if (!PAIR) tmem_ld16(lanes + 256 + (s ^ 1) * 128 + cb, b);
+                tmem_wait_ld();
+                float v[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    v[u] = __uint_as_float(a[u]);
+                    if (!PAIR)  // a stream without a key of this row holds no values
+                        v[u] = (w0 != 0.f ? w0 * v[u] : 0.f) + (w1 != 0.f ? w1 * __uint_as_float(b[u]) : 0.f);
+                }
+                if (live && bad) {
+                    // infinities and NaN of drafted rows this node attends
+                    for (unsigned long long rest = bad; rest; rest &= rest - 1) {
+                        const int r = ud->L + __ffsll((long long)rest) - 1;
+                        const int page = p.table[(size_t)ud->b * p.max_pages + (r >> p.page_shift)];
+                        const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.vc) +
+                                                  (((size_t)page * p.Hkv + kvh) * p.page_size + (r & (p.page_size - 1))) * D + cb;
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) {
+                            const float f = __bfloat162float(vr[u]);
+                            if (!(fabsf(f) < INFINITY)) v[u] += f;
+                        }
+                    }
+                }
+                if (live && whole) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        *reinterpret_cast<uint4*>(orow + cb + q * 8) =
+                            make_uint4(pack_bf16x2(v[8 * q] * inv, v[8 * q + 1] * inv), pack_bf16x2(v[8 * q + 2] * inv, v[8 * q + 3] * inv),
+                                       pack_bf16x2(v[8 * q + 4] * inv, v[8 * q + 5] * inv), pack_bf16x2(v[8 * q + 6] * inv, v[8 * q + 7] * inv));
+                } else if (live) {
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) *reinterpret_cast<float2*>(part + cb + u) = make_float2(v[u], v[u + 1]);
+                }
+            }
+            if (live && !whole && (PAIR || s == 0))
+                *reinterpret_cast<float2*>(part + D) = make_float2(ref == kNoRef ? -INFINITY : ref, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.ufree[nu & 1]);
+            named_sync(bid, 256);  // O and xch are read before the next unit overwrites them
+            ro.unit_done(nu);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int NROWS>
+cudaError_t run_one(const PagedProblem& p, const Launch& ln, cudaStream_t st, int* grid)
+{
+    CUtensorMap tk, tv;
+    cudaError_t e;
+    const int planes = p.num_pages * p.Hkv, box = std::min(p.page_size, KT);
+    if ((e = tc::make_map(&tk, p.kc, D, p.page_size, p.page_size, planes, box)) != cudaSuccess) return e;
+    if ((e = tc::make_map(&tv, p.vc, D, p.page_size, p.page_size, planes, box)) != cudaSuccess) return e;
+    constexpr int smem = RowCfg<D, NROWS>::TOTAL;
+    auto kern = decode_paged_rows_kernel<D, NROWS>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    int dev = 0, nsm = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    *grid = std::min(nsm, kTcCtas);
+    kern<<<*grid, 512, smem, st>>>(tk, tv, p, ln);
+    return cudaGetLastError();
+}
+
+cudaError_t run_rows(const PagedProblem& p, int d, int rows, const Launch& ln, cudaStream_t st, int* grid)
+{
+    if (d == 64) return rows <= 128 ? run_one<64, 128>(p, ln, st, grid) : run_one<64, 256>(p, ln, st, grid);
+    return rows <= 128 ? run_one<128, 128>(p, ln, st, grid) : run_one<128, 256>(p, ln, st, grid);
+}
+
+}  // namespace ptc
+
+// Query rows of a unit: the smallest capacity that holds a request's rows of one kv
+// head, 256 for more (several units then).
+int paged_tc_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
+
+size_t paged_tc_workspace(int rows, int d)
+{
+    return (size_t)ptc::kTcCtas * 2 * paged_tc_rows(rows) * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s, int* grid)
+{
+    const ptc::Launch ln{p.dev_error, p.wait_cycles > 0 ? p.wait_cycles : kPrefillWaitCycles, p.inject, 1};
+    const int rows = paged_tc_rows(p.max_nodes * p.group);
+    return rows <= 32 ? ptc::run_cols(p, d, rows, ln, s, grid) : ptc::run_rows(p, d, rows, ln, s, grid);
+}
+
+}  // namespace jl

@@ -72,7 +72,7 @@ cudaError_t launch_block_tables(const TablesProblem& p, cudaStream_t s, int* nla
 cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t s, int* nlaunch);
 cudaError_t launch_tree_commit(const CommitProblem& p, cudaStream_t s, int* nlaunch);
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_nodes);
-int paged_tc_columns(int rows);
+int paged_tc_rows(int rows);
 size_t paged_tc_workspace(int rows, int d);
 cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s, int* grid);
 cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch);

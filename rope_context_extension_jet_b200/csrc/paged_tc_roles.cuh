@@ -1,0 +1,716 @@
+// paged_tc_roles.cuh -- the warp roles that both tensor-core kernels of the paged
+// decode share: the producers of key and value tiles, the planner of units, and
+// the rotation of keys and queries.  A kernel's configuration C lays out shared
+// memory and says how many threads share a tile.
+//
+// Every wait on a barrier is bounded (an mbarrier wait gives up after a limit,
+// records a code in the device error word and sets the CTA's abort flag, which
+// ends every other wait); warps that meet at a named barrier agree there whether
+// any of them gave up, so none is left waiting at it.
+#pragma once
+
+#include "paged_common.cuh"
+#include "prefill_tc_common.cuh"
+
+namespace jl {
+namespace ptc {
+
+constexpr int KT = 128;
+constexpr int kTcCtas = 148;
+// Reference of a query row (log2 units): its largest logit so far plus kAbove when it
+// was last set; it is set again once a logit passes it by kExceed.  Weights then lie
+// in (0, 2^kExceed], the largest of them at 2^-kAbove or above: fp32 and bf16 keep
+// their relative precision over all of that, a weight 2^-100 of the largest is still
+// a normal number, and only a logit that beats everything before it by 40 octaves
+// costs a rescale.
+constexpr float kAbove = 24.f, kExceed = 16.f;
+constexpr float kNoRef = -1e30f;    // reference of a row before its first key
+constexpr int UNITS = 4;            // ring of units planned ahead
+constexpr int INFO = 8;             // ring of per-item notes: a role is at most NSK + 2 items ahead of another
+// A unit of this CTA's piece, as the planner leaves it in shared memory for the
+// other roles (read there field by field: registers are scarce).
+struct UnitDesc {
+    int rows;            // query rows; 0: no more units
+    int L, T, n0, b;     // committed rows, nodes, first token row, request
+    int kvh, r0;         // kv head, first query row
+    int i0, i1;          // its items in this piece
+    int gmin, ng, nR, kE0, w0, items;
+    int pad;
+};
+typedef const volatile UnitDesc* UnitPtr;
+
+struct Launch {
+    int* dev_error;
+    long long wait_cycles;
+    int inject, min_items;
+};
+
+// Up to 32 query rows per unit: decode_paged_tc.cu; more: decode_paged_rows.cu.
+cudaError_t run_cols(const PagedProblem& p, int d, int cols, const Launch& ln, cudaStream_t st, int* grid);
+cudaError_t run_rows(const PagedProblem& p, int d, int rows, const Launch& ln, cudaStream_t st, int* grid);
+
+// Shared memory after the tiles, from offset BASE: notes of two units (per query
+// row: ancestors, position - w0, group size, logit scale; per node: depth), scratch
+// of the unit set-up, rings of per-item notes, the plan and the barriers.
+template <int D, int ROWS, int NSK, int NSV, int BASE, int EXTRA_BARS, int WARPS>
+struct Notes {
+    static constexpr int UNIT = BASE;
+    static constexpr int U_ANC = 0, U_DEPTH = U_ANC + ROWS * 8, U_LIM = U_DEPTH + kMaxNodes * 4, U_QG = U_LIM + ROWS * 4;
+    static constexpr int U_CQ = U_QG + ROWS * 4, U_BAD = U_CQ + ROWS * 4, UBYTES = U_BAD + 16;
+    static constexpr int QS = UNIT + 2 * UBYTES;            // [ROWS] query scales, [ROWS] positions
+    static constexpr int PAR = QS + ROWS * 8;               // [64] parents, [64] node ancestors
+    static constexpr int KSC = PAR + kMaxNodes * 12;        // [INFO][128] inverse key scales
+    static constexpr int TURNS = KSC + INFO * KT * 4;       // [D / 2] phase constants (hi, lo)
+    static constexpr int NOTE = TURNS + D / 2 * 8;          // [INFO] mask of the pages present
+    static constexpr int SCALED = NOTE + INFO * 4;          // [INFO][4] a rotation warp scaled rows of the tile
+    static constexpr int PLAN = SCALED + INFO * 16;
+    static constexpr int DESC = PLAN + (int)sizeof(PiecePlan);
+    static constexpr int SCAN = DESC + UNITS * (int)sizeof(UnitDesc);
+    static constexpr int BAR = SCAN + (WARPS + 1) * 8;
+    static constexpr int NBARS = 3 * NSK + 3 * NSV + 5 + 1 + 2 * UNITS + EXTRA_BARS;
+    static constexpr int SLOT = BAR + NBARS * 8;            // TMEM address, abort flag
+    static constexpr int NOTES_END = (SLOT + 16 + 15) / 16 * 16;
+    static_assert(INFO > NSK + 1, "ring of per-item notes");
+};
+
+// The barriers, in the order of their use.
+template <class C>
+struct Bars {
+    uint64_t *kfull, *kready, *kempty;  // key tile landed; rotated; read by the tensor cores
+    uint64_t *vfull, *vfix, *vempty;    // value tile landed; cleared where rows are missing; read
+    uint64_t *uready, *ufree;           // notes of unit k (two buffers) written; done with
+    uint64_t *qready;                   // queries of a phase rotated
+    uint64_t *dfull, *dfree;            // unit planned; done with
+    uint64_t *drain, *extra;
+    __device__ __forceinline__ explicit Bars(unsigned char* smem)
+    {
+        kfull = reinterpret_cast<uint64_t*>(smem + C::BAR);
+        kready = kfull + C::NSK;
+        kempty = kready + C::NSK;
+        vfull = kempty + C::NSK;
+        vfix = vfull + C::NSV;
+        vempty = vfix + C::NSV;
+        uready = vempty + C::NSV;
+        ufree = uready + 2;
+        qready = ufree + 2;
+        dfull = qready + 1;
+        dfree = dfull + UNITS;
+        drain = dfree + UNITS;
+        extra = drain + 1;
+    }
+    // one thread; C::ROT threads rotate a tile, C::ROTALL in all, C::SOFT softmax warps
+    __device__ __forceinline__ void init()
+    {
+        for (int s = 0; s < C::NSK; ++s) {
+            mbar_init(&kfull[s], 1);
+            mbar_init(&kready[s], C::ROT / 32);
+            mbar_init(&kempty[s], 1);
+        }
+        for (int s = 0; s < C::NSV; ++s) {
+            mbar_init(&vfull[s], 1);
+            mbar_init(&vfix[s], C::ROT / 32);
+            mbar_init(&vempty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&uready[s], C::ROTALL / 32);
+            mbar_init(&ufree[s], C::SOFT);
+        }
+        mbar_init(qready, C::ROTALL / 32);
+        for (int s = 0; s < UNITS; ++s) {
+            mbar_init(&dfull[s], 1);
+            mbar_init(&dfree[s], 3 + C::ROTALL / 32 + C::SOFT);  // two producers, the issuer, rotation, softmax
+        }
+        mbar_init(drain, 1);
+    }
+};
+
+// The items of a unit in order: the group size its keys are aliased by (0: exact
+// positions) and the key tile.
+struct UnitItems {
+    int g, tile, left;
+    __device__ __forceinline__ explicit UnitItems(UnitPtr u)
+    {
+        const int i = u->i0, nR = u->nR, rem = u->ng * nR;
+        left = u->i1 - i;
+        g = 0;
+        tile = u->kE0 + (i - rem);
+        if (i < rem) {
+            g = u->gmin + i / nR;
+            tile = i % nR;
+        }
+    }
+    __device__ __forceinline__ void next(UnitPtr u)
+    {
+        --left;
+        ++tile;
+        if (g != 0 && tile == u->nR) {
+            const bool more = g + 1 < u->gmin + u->ng;
+            tile = more ? 0 : u->kE0;
+            g = more ? g + 1 : 0;
+        }
+    }
+};
+
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool named_or(int id, int n, bool x)
+{
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((int)x), "r"(id), "r"(n) : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Bounded wait of a whole warp on a barrier phase, as tc::warp_wait, but the
+// hardware may park the warp for up to kParkNs per try: polling warps would take
+// issue slots from the ones at work (the largest trees ran at half their speed).
+constexpr uint32_t kParkNs = 100000;
+__device__ __forceinline__ bool try_wait_parked(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* dev_error, long long limit,
+                                          int code)
+{
+    bool ok = try_wait_parked(bar, parity);
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = try_wait_parked(bar, parity))) {
+            if (*abort_flag) break;
+            if (clock64() - t0 > limit) {
+                record_error(dev_error, code);
+                *abort_flag = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+
+// One MMA (one thread issues): D[tmem] (+)= A B, operands in shared memory.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t mag16(uint32_t a) { return max(a & 0x7fffu, (a >> 16) & 0x7fffu); }
+
+// What every role sees.
+template <class C>
+struct Role {
+    const PagedProblem& p;
+    const Launch& ln;
+    unsigned char* smem;
+    Bars<C> bars;
+    volatile int* abort_flag;
+    int warp, lane;
+    __device__ __forceinline__ Role(const PagedProblem& p_, const Launch& ln_, unsigned char* smem_)
+        : p(p_), ln(ln_), smem(smem_), bars(smem_)
+    {
+        abort_flag = reinterpret_cast<volatile int*>(smem + C::SLOT + 4);
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
+    }
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int code) const
+    {
+        return warp_wait(bar, parity, abort_flag, ln.dev_error, ln.wait_cycles, code);
+    }
+    // unit k of the piece: wait until it is planned; afterwards each warp hands it back
+    __device__ __forceinline__ bool unit_wait(int k, int code) const { return wait(&bars.dfull[k % UNITS], (k / UNITS) & 1, code); }
+    __device__ __forceinline__ UnitPtr unit(int k) const { return reinterpret_cast<UnitDesc*>(smem + C::DESC) + k % UNITS; }
+    __device__ __forceinline__ void unit_done(int k) const
+    {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.dfree[k % UNITS]);
+    }
+    __device__ __forceinline__ volatile unsigned* note() const { return reinterpret_cast<volatile unsigned*>(smem + C::NOTE); }
+    __device__ __forceinline__ unsigned all_pages() const { return (1u << (KT >> min(p.page_shift, 7))) - 1; }
+};
+
+// Start of a CTA: barriers, tensor memory (warp 2), the plan of its piece.  Returns
+// the tensor memory address.
+template <class C, uint32_t TCOLS, class InitExtra>
+__device__ __forceinline__ uint32_t start_cta(const Role<C>& ro, InitExtra init_extra)
+{
+    uint32_t* slot = reinterpret_cast<uint32_t*>(ro.smem + C::SLOT);
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        Bars<C> bars(ro.smem);
+        bars.init();
+        init_extra();
+        *ro.abort_flag = *reinterpret_cast<volatile int*>(ro.ln.dev_error) != 0;  // an earlier wait ran out: no work
+        fence_mbar_init();
+    }
+    for (int m = tid; m < C::DIM / 2; m += C::THREADS)
+        reinterpret_cast<uint2*>(ro.smem + C::TURNS)[m] = make_uint2(ro.p.turns.hi[m], ro.p.turns.lo[m]);
+    if (ro.warp == 2) {
+        tmem_alloc(slot, TCOLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    // ends with a barrier of the CTA
+    piece_plan<KT, C::ROWS, C::THREADS>(ro.p, ro.ln.min_items, reinterpret_cast<PiecePlan*>(ro.smem + C::PLAN),
+                                        reinterpret_cast<long long*>(ro.smem + C::SCAN));
+    tc_fence_after();
+    return *slot;
+}
+
+// Producer of key tiles (warp 0) or value tiles (warp 3): the page numbers of a
+// tile's rows, then one TMA box per page and 64 columns.
+template <class C, bool isK>
+__device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm)
+{
+    const PagedProblem& p = ro.p;
+    const Launch& ln = ro.ln;
+    unsigned char* smem = ro.smem;
+    const int lane = ro.lane;
+    constexpr int D = C::DIM;
+        constexpr int NS = isK ? C::NSK : C::NSV;
+    uint64_t* full = isK ? ro.bars.kfull : ro.bars.vfull;
+    uint64_t* empty = isK ? ro.bars.kempty : ro.bars.vempty;
+        unsigned char* ring = smem + (isK ? C::K0 : C::V0);
+    const int box = min(p.page_size, KT);
+    int e = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        if (!ro.unit_wait(k, 0x403)) break;
+        UnitPtr un = ro.unit(k);
+        if (un->rows == 0) break;
+        const int* table = p.table + (size_t)un->b * p.max_pages;
+        const int n = un->L + un->T, kvh = un->kvh;
+        for (UnitItems it(un); it.left > 0; it.next(un), ++e) {
+            // lane x looks after rows [x box, (x + 1) box) of the tile
+            const int row = it.tile * KT + lane * box;
+            const bool want = lane * box < KT && row < n;
+            int page = -1;
+            if (want) {
+                page = __ldg(table + (row >> p.page_shift));
+                if ((unsigned)page >= (unsigned)p.num_pages) {
+                    record_input(p.input_error, kBadPage);
+                    page = -1;
+                }
+            }
+            const int st = e % NS;
+            if (e >= NS && !ro.wait(&empty[st], ((e / NS) - 1) & 1, isK ? 0x401 : 0x402)) { ok = false; break; }
+            const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+            const bool skip = isK && e == 0 && ln.inject == kInjectDecodeCopy;  // test hook: the first key tile is never loaded
+            if (lane == 0) {
+                if (isK) ro.note()[e % INFO] = have;
+                if (!skip) {
+                    if (have)
+                        mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(have) * box * D * 2));
+                    else
+                        mbar_arrive(&full[st]);
+                }
+            }
+            __syncwarp();
+            if (page >= 0 && !skip) {
+                unsigned char* dst = ring + st * C::TILE + lane * box * 128;
+                const int y = row & (p.page_size - 1), z = page * p.Hkv + kvh;
+#pragma unroll
+                for (int a = 0; a < C::ATOMS; ++a) tma_load_3d(dst + a * C::ATOM_K, tm, a * 64, y, z, &full[st]);
+            }
+        }
+        ro.unit_done(k);
+    }
+    // the copies in flight land before the CTA ends
+    for (int x = max(0, e - NS); x < e; ++x)
+        if (!(isK && x == 0 && ln.inject == kInjectDecodeCopy)) mbar_wait(&full[x % NS], (x / NS) & 1);
+}
+
+// Planner (one thread of warp 2): the units of this CTA's piece, a few ahead.
+template <class C>
+__device__ __forceinline__ void plan_units(const Role<C>& ro)
+{
+    const PagedProblem& p = ro.p;
+    const PiecePlan* plan = reinterpret_cast<const PiecePlan*>(ro.smem + C::PLAN);
+    if (ro.lane == 0) {
+        clear_cut(p);
+        long long cur = plan->start, base = plan->base;
+        const long long end = *ro.abort_flag ? cur : plan->end;
+        int b = plan->b, k = 0;
+        for (;; ++k) {
+            UnitDesc u;
+            u.rows = 0;
+            if (cur < end) {
+                SeqPlan s = seq_plan<KT, C::ROWS>(p, b, false);
+                long long cnt = (long long)s.items * s.row_tiles * p.Hkv;
+                while (cur >= base + cnt) {
+                    base += cnt;
+                    ++b;
+                    s = seq_plan<KT, C::ROWS>(p, b, false);
+                    cnt = (long long)s.items * s.row_tiles * p.Hkv;
+                }
+                int unit;
+                div_items(cur - base, s.items, &unit, &u.i0);
+                u.i1 = (int)min((long long)s.items, u.i0 + (end - cur));
+                u.kvh = unit / s.row_tiles;
+                u.r0 = (unit % s.row_tiles) * C::ROWS;
+                u.rows = min(C::ROWS, s.T * p.group - u.r0);
+                u.L = s.L;
+                u.T = s.T;
+                u.n0 = s.n0;
+                u.b = b;
+                u.gmin = s.gmin;
+                u.ng = s.ng;
+                u.nR = s.nR;
+                u.kE0 = s.kE0;
+                u.w0 = s.w0;
+                u.items = s.items;
+                if (u.i0 == 0 && u.i1 < s.items) note_cut(p, s, plan->per, cur, u.kvh, u.r0, u.rows);
+                cur += u.i1 - u.i0;
+            }
+            if (k >= UNITS && !tc::wait_or_abort(&ro.bars.dfree[k % UNITS], ((k / UNITS) - 1) & 1, ro.abort_flag, ro.ln.dev_error, ro.ln.wait_cycles, 0x441))
+                break;
+            reinterpret_cast<UnitDesc*>(ro.smem + C::DESC)[k % UNITS] = u;
+            mbar_arrive(&ro.bars.dfull[k % UNITS]);
+            if (u.rows == 0) break;
+        }
+    }
+    __syncwarp();
+}
+
+// Rotation (C::ROTALL threads from thread 128 on).  Per unit: the tree, positions and
+// query scales.  Per phase: the queries rotated into shared memory.  Per tile: the
+// keys rotated in place; on a request's last tiles the value rows that do not exist
+// are cleared.
+template <class C>
+__device__ __forceinline__ void rotate_keys(const Role<C>& ro)
+{
+    const PagedProblem& p = ro.p;
+    unsigned char* smem = ro.smem;
+    const int lane = ro.lane;
+    constexpr int D = C::DIM, H = D / 2, CH = D / 16, NSK = C::NSK, NSV = C::NSV;
+    float* ksc = reinterpret_cast<float*>(smem + C::KSC);
+        const int t = (int)threadIdx.x - 128, rt = t & (C::ROT - 1);  // thread of the role, of the tile
+    const int group = C::ALT ? t >> 7 : 0;
+    constexpr int RPT = KT * CH / C::ROT;          // rows per thread of a tile: 128 rows x CH chunk pairs
+    const int c = t % CH, row0 = (rt / CH) * RPT;
+    const uint4* turns = reinterpret_cast<const uint4*>(smem + C::TURNS) + c * 4;  // the thread's 8 frequencies
+    float2 stc[4], sts[4];                         // cos, sin of one position step, as frequency pairs
+    auto angles = [&](uint32_t f, float2 (&cs)[4], float2 (&sn)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint4 w2 = turns[u];
+            rope_cs_fast(f, w2.x, w2.y, cs[u].x, sn[u].x);
+            rope_cs_fast(f, w2.z, w2.w, cs[u].y, sn[u].y);
+        }
+    };
+    angles(1u, stc, sts);
+    // 8 pairs (lo.x holds dimensions 0, 1 of the chunk, hi.x their partners, ...)
+    // turned by (cs, sn), as fp16
+    auto turn = [&](uint4& lo, uint4& hi, const float2 (&cs)[4], const float2 (&sn)[4]) {
+        uint32_t* a = &lo.x;
+        uint32_t* b = &hi.x;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float2 x = make_float2(bf16_lo(a[u]), bf16_hi(a[u])), y = make_float2(bf16_lo(b[u]), bf16_hi(b[u]));
+            const float2 ny = make_float2(__uint_as_float((b[u] << 16) + 0x80000000u),
+                                          __uint_as_float((b[u] & 0xffff0000u) ^ 0x80000000u));
+            const float2 r0 = fma2(ny, sn[u], mul2(x, cs[u])), r1 = fma2(y, cs[u], mul2(x, sn[u]));
+            a[u] = pack_f16x2(r0.x, r0.y);
+            b[u] = pack_f16x2(r1.x, r1.y);
+        }
+    };
+    auto absmax8 = [](const uint4& a, const uint4& b) {
+        return absmax2(absmax2(absmax2(a.x, a.y), absmax2(a.z, a.w)), absmax2(absmax2(b.x, b.y), absmax2(b.z, b.w)));
+    };
+    auto scale8 = [](uint4& a, float sc) {  // exact: a power of two (elements far below the row's largest may vanish)
+        a.x = pack_bf16x2(bf16_lo(a.x) * sc, bf16_hi(a.x) * sc);
+        a.y = pack_bf16x2(bf16_lo(a.y) * sc, bf16_hi(a.y) * sc);
+        a.z = pack_bf16x2(bf16_lo(a.z) * sc, bf16_hi(a.z) * sc);
+        a.w = pack_bf16x2(bf16_lo(a.w) * sc, bf16_hi(a.w) * sc);
+    };
+    const int gshift = min(p.page_shift, 7);
+    const unsigned all_pages = (1u << (KT >> gshift)) - 1;
+    int* par = reinterpret_cast<int*>(smem + C::PAR);
+    unsigned long long* nanc = reinterpret_cast<unsigned long long*>(par + kMaxNodes);
+    float* qsc = reinterpret_cast<float*>(smem + C::QS);
+    int* qpos = reinterpret_cast<int*>(qsc + C::ROWS);
+    int e = 0, nu = 0;
+    // A wait that runs out in one warp must not leave the others at a barrier:
+    // the warps meet once per unit (and once after the last) and stop together
+    // if any of them gave up.
+    bool ok = true, agreed = false;
+    for (; ok; ++nu) {
+        ok = ro.unit_wait(nu, 0x426);
+        UnitPtr ud = ro.unit(nu);
+        if (ok && ud->rows == 0) break;
+        unsigned char* un = smem + C::UNIT + (nu & 1) * C::UBYTES;
+        int* depth = reinterpret_cast<int*>(un + C::U_DEPTH);
+        int* lim0 = reinterpret_cast<int*>(un + C::U_LIM);
+        int* qG = reinterpret_cast<int*>(un + C::U_QG);
+        float* cq = reinterpret_cast<float*>(un + C::U_CQ);
+        unsigned long long* canc = reinterpret_cast<unsigned long long*>(un + C::U_ANC);
+        unsigned long long* bad = reinterpret_cast<unsigned long long*>(un + C::U_BAD);
+        int* big = reinterpret_cast<int*>(bad + 1);
+        // the softmax is done with unit nu - 2, the tensor cores with the
+        // queries of unit nu - 1
+        ok = ok && (nu < 2 || ro.wait(&ro.bars.ufree[nu & 1], ((nu >> 1) - 1) & 1, 0x421)) &&
+             (e == 0 || ro.wait(&ro.bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x422));
+        if ((agreed = named_or(1, C::ROTALL, !ok))) break;
+        const int L = ud->L, T = ud->T, n = L + T, rows = ud->rows, r0 = ud->r0, kvh = ud->kvh;
+        if (t < T) {
+            int x = t - 1;
+            if (p.parents) {
+                x = p.parents[ud->n0 + t];
+                if (x < -1 || x >= t) {
+                    record_input(p.input_error, kBadParent);
+                    x = -1;
+                }
+            }
+            par[t] = x;
+        }
+        if (t == 0) {
+            *bad = 0;
+            *big = 0;
+        }
+        named_sync(1, C::ROTALL);
+        if (t < T) {
+            unsigned long long m = (2ull << t) - 1;
+            if (p.parents) {
+                m = 0;
+                for (int x = t; x >= 0; x = par[x]) m |= 1ull << x;
+            }
+            nanc[t] = m;
+            depth[t] = __popcll(m) - 1;
+        }
+        named_sync(1, C::ROTALL);
+        for (int row = t; row < C::ROWS; row += C::ROTALL) {
+            int x = 0, G = 0;
+            float inv = 0.f, sc = 0.f;
+            unsigned long long up = 0;
+            if (row < rows) {
+                const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
+                x = L + depth[node];
+                G = x / p.w_pre + 1;
+                up = nanc[node];
+                // the query times a power of two that brings its largest element
+                // into [2^13, 2^14); the logits times the inverse
+                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                                ((size_t)(ud->n0 + node) * p.Hq + hd) * D);
+                uint32_t mx = 0;
+                float l1 = 0.f;
+#pragma unroll 4
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 v = q[k];
+                    mx = absmax2(mx, absmax2(absmax2(v.x, v.y), absmax2(v.z, v.w)));
+                    l1 += fabsf(bf16_lo(v.x)) + fabsf(bf16_hi(v.x)) + fabsf(bf16_lo(v.y)) + fabsf(bf16_hi(v.y)) +
+                          fabsf(bf16_lo(v.z)) + fabsf(bf16_hi(v.z)) + fabsf(bf16_lo(v.w)) + fabsf(bf16_hi(v.w));
+                }
+                const int ex = tc::range_exp(mag16(mx));
+                sc = tc::pow2i(ex);
+                inv = fminf(fmaxf(tc::pow2i(-ex) * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);  // a normal number: -inf times it stays -inf
+                // keys rounded to fp16 as they are err by up to 2^-25 where fp16 is
+                // subnormal; with an L1 norm this large that could reach 2^-11 of a logit
+                if (!(l1 * p.scale_log2 * 1.4142136f <= 16384.f)) *big = 1;
+            }
+            qpos[row] = x;
+            lim0[row] = x - ud->w0;
+            qG[row] = G;
+            canc[row] = up;
+            cq[row] = inv;
+            qsc[row] = sc;
+        }
+        named_sync(1, C::ROTALL);
+        if (lane == 0) mbar_arrive(&ro.bars.uready[nu & 1]);
+        const bool always = *big != 0;
+        int gcur = -1;
+        uint32_t dm = 0, ds1 = 0, ds2 = 0;  // division by the group size by multiply-shift
+        for (UnitItems it(ud); it.left > 0; it.next(ud), ++e) {
+            const int g = it.g;
+            if (g != gcur) {
+                // queries of this phase; the tensor cores are done with those of the last
+                if (gcur >= 0 && !ro.wait(&ro.bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423)) { ok = false; break; }
+                gcur = g;
+                const uint32_t dv = max(g, 1);
+                const uint32_t lg = 32 - __clz(dv - 1);  // ceil(log2 dv); 0 for 1
+                dm = (uint32_t)(((((uint64_t)1 << 32) * (((uint64_t)1 << lg) - dv)) / dv) + 1);
+                ds1 = min(lg, 1u);
+                ds2 = lg > 1 ? lg - 1 : 0;
+#pragma unroll 1
+                for (int x = t; x < C::ROWS * CH; x += C::ROTALL) {
+                    const int r = x / CH;  // CH divides the thread count: chunk x % CH = c
+                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                    if (r < rows) {
+                        const int node = (r0 + r) / p.group, hd = kvh * p.group + (r0 + r) % p.group;
+                        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
+                                                 ((size_t)(ud->n0 + node) * p.Hq + hd) * D;
+                        lo = *reinterpret_cast<const uint4*>(q + c * 8);
+                        hi = *reinterpret_cast<const uint4*>(q + H + c * 8);
+                        float2 cs[4], sn[4];
+                        angles((uint32_t)qpos[r] / dv, cs, sn);
+                        const float2 sc = make_float2(qsc[r], qsc[r]);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            cs[u] = mul2(cs[u], sc);
+                            sn[u] = mul2(sn[u], sc);
+                        }
+                        turn(lo, hi, cs, sn);
+                    }
+                    *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(r, c)) = lo;
+                    *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(r, c + CH)) = hi;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ro.bars.qready);
+            }
+            if (C::ALT && (e & 1) != group) continue;
+            const int st = e % NSK, j0 = it.tile * KT;
+            unsigned char* kt = smem + C::K0 + st * C::TILE;
+            const bool drafted = j0 + KT > L;
+            // turned position of a row: its place, or a drafted row's depth, over the
+            // group size (rows past the end: 0, they are masked)
+            auto turned = [&](int r) {
+                const int j = j0 + r;
+                uint32_t pos = (uint32_t)j;
+                if (drafted && j >= L) pos = j < n ? (uint32_t)(L + depth[j - L]) : 0u;
+                const uint32_t t1 = __umulhi(dm, pos);
+                return (t1 + ((pos - t1) >> ds1)) >> ds2;
+            };
+            uint32_t f = turned(row0);
+            float2 cs[4], sn[4];
+            angles(f, cs, sn);
+            unsigned scaled = 0;
+            if (!ro.wait(&ro.bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
+            // from row to row the turned position stays or steps by one (drafted
+            // rows may jump): the angles follow by the angle addition
+            auto advance = [&](int r) {
+                const uint32_t fn = turned(r);
+                if (fn == f + 1) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float2 ns = make_float2(-sn[u].x, -sn[u].y);
+                        const float2 nc = fma2(ns, sts[u], mul2(cs[u], stc[u]));
+                        sn[u] = fma2(cs[u], sts[u], mul2(sn[u], stc[u]));
+                        cs[u] = nc;
+                    }
+                } else if (fn != f) {
+                    angles(fn, cs, sn);
+                }
+                f = fn;
+            };
+#pragma unroll 1
+            for (int x = 0; x < RPT; x += 2) {
+                const int r = row0 + x;
+                uint4* pa = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c));
+                uint4* pb = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c + CH));
+                uint4* pc = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r + 1, c));
+                uint4* pd = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r + 1, c + CH));
+                uint4 a0 = *pa, b0 = *pb, a1 = *pc, b1 = *pd;
+                // Keys are rounded to fp16 as they are, unless one of the warp's is too
+                // large for it (0x4700: 2^15), or the query makes small ones count: then
+                // every row is first scaled by its own power of two.
+                uint32_t m0 = absmax8(a0, b0), m1 = absmax8(a1, b1);
+                float k0 = 1.f, k1 = 1.f;
+                if (__any_sync(0xffffffffu, always || mag16(absmax2(m0, m1)) >= 0x4700u)) {
+                    scaled = 1;
+                    m0 = mag16(m0);
+                    m1 = mag16(m1);
+#pragma unroll
+                    for (int o = 1; o < CH; o <<= 1) {
+                        m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                        m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                    }
+                    const int e0 = tc::range_exp(m0), e1 = tc::range_exp(m1);
+                    scale8(a0, tc::pow2i(e0));
+                    scale8(b0, tc::pow2i(e0));
+                    scale8(a1, tc::pow2i(e1));
+                    scale8(b1, tc::pow2i(e1));
+                    k0 = tc::pow2i(-e0);
+                    k1 = tc::pow2i(-e1);
+                }
+                if (c == 0) *reinterpret_cast<float2*>(ksc + (e % INFO) * KT + r) = make_float2(k0, k1);
+                if (x > 0) advance(r);
+                turn(a0, b0, cs, sn);
+                *pa = a0;
+                *pb = b0;
+                advance(r + 1);
+                turn(a1, b1, cs, sn);
+                *pc = a1;
+                *pd = b1;
+            }
+            if (lane == 0) reinterpret_cast<volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 4 + (rt >> 5)] = scaled;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ro.bars.kready[st]);
+            // value rows that do not exist count as zero: the page may hold
+            // anything there, and a weight of 0 does not silence NaN.  A drafted
+            // row's own infinities and NaN are cleared as well (nodes beside it
+            // must not see them) and noted for the nodes that do attend it.
+            const unsigned have = ro.note()[e % INFO];
+            if (drafted || have != all_pages) {
+                const int sv = e % NSV;
+                if (!ro.wait(&ro.bars.vfull[sv], (e / NSV) & 1, 0x425)) { ok = false; break; }
+                unsigned char* vt = smem + C::V0 + sv * C::TILE;
+                constexpr int TPR = C::ROT / KT;  // threads per row
+                const int r = rt / TPR, j = j0 + r;
+                const bool there = j < n && ((have >> (r >> gshift)) & 1);
+                if (!there || j >= L) {
+#pragma unroll 1
+                    for (int k = rt % TPR; k < D / 8; k += TPR) {
+                        uint4* v = reinterpret_cast<uint4*>(vt + tc::sw128_off<KT>(r, k));
+                        if (!there) {
+                            *v = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint4 x = *v;
+                        uint32_t* y = &x.x;
+                        bool hit = false;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if ((y[u] & 0x7f80u) == 0x7f80u) { y[u] &= 0xffff0000u; hit = true; }
+                            if ((y[u] & 0x7f800000u) == 0x7f800000u) { y[u] &= 0xffffu; hit = true; }
+                        }
+                        if (hit) {
+                            *v = x;
+                            atomicOr(bad, 1ull << (j - L));
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ro.bars.vfix[sv]);
+            }
+        }
+        ro.unit_done(nu);
+    }
+    if (!agreed) named_or(1, C::ROTALL, !ok);
+}
+
+}  // namespace ptc
+}  // namespace jl
