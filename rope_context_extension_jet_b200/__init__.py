@@ -160,7 +160,7 @@ def _dev(t, name):
 
 def _like(t, ref, name, ref_name):
     """The library writes ``t`` with ``ref``'s shape and element type."""
-    if tuple(t.shape) != tuple(ref.shape) or t.dtype != ref.dtype:
+    if t.shape != ref.shape or t.dtype != ref.dtype:
         raise ValueError(f"{name} must match {ref_name}: shape {tuple(ref.shape)}, dtype {ref.dtype} "
                          f"(got {tuple(t.shape)}, {t.dtype})")
 
@@ -410,14 +410,38 @@ def decode_noalloc(q, kcache, vcache, L: int, out=None, *, w0: int, w_pretrained
 # step (block_tables, cache_append, decode_paged or decode_tree, tree_commit) can
 # be captured into a CUDA graph.
 
-def _ints(t, name, shape, optional=False):
-    """Device pointer of an int32 array of the given shape (None where optional)."""
+def _current():
+    """(current device, its current stream's handle): looked up once per call, by the
+    raw queries (the public ones build objects, at a few microseconds a call, and a
+    decode step is a few microseconds long)."""
     import torch
-    if t is None and optional:
+    if not torch.cuda.is_initialized():
+        return -2, None  # then no tensor is on a device either: the argument checks say so
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _ptr(t, name, dev):
+    """Device pointer of a contiguous tensor on device ``dev`` (checks as ``_dev``)."""
+    if t.get_device() != dev or not t.is_contiguous():
+        return _dev(t, name)
+    return t.data_ptr()
+
+
+def _ints(t, name, shape, dev):
+    """Device pointer of an int32 array of the given shape (None stays None)."""
+    import torch
+    if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+    if t.dtype is not torch.int32 or t.shape != shape:
         raise ValueError(f"{name} must be an int32 tensor of shape {tuple(shape)} (got {t.dtype}, {tuple(t.shape)})")
-    return _dev(t, name)
+    return _ptr(t, name, dev)
+
+
+def _need(t, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return t
 
 
 def _caches(kcache, vcache):
@@ -455,32 +479,31 @@ def block_tables(lens, grow, block_table, held, free_list, free_count, *, page_s
     row_start = torch.empty(B + 1, dtype=i32, device=dev) if row_start is None else row_start
     status = torch.empty(B, dtype=i32, device=dev) if status is None else status
     lib = load_library()
+    cur, raw = _current()
     _check(lib.jetlong_block_tables(
-        _ints(lens, "lens", (B,)), _ints(grow, "grow", (B,)), _ints(release, "release", (B,), True),
-        _ints(held, "held", (B,)), _ints(free_count, "free_count", (1,)),
-        _ints(block_table, "block_table", (B, max_pages)), _ints(free_list, "free_list", (free_list.shape[0],)),
-        _ints(lens_out, "lens_out", (B,)), _ints(held_out, "held_out", (B,)),
-        _ints(free_count_out, "free_count_out", (1,)), _ints(slot_map, "slot_map", (n_rows,)),
-        _ints(row_start, "row_start", (B + 1,)), _ints(status, "status", (B,)), B, max_pages, int(page_size),
-        int(num_pages), free_list.shape[0], int(n_rows), _stream(stream)), lib)
+        _ints(_need(lens, "lens"), "lens", (B,), cur), _ints(_need(grow, "grow"), "grow", (B,), cur),
+        _ints(release, "release", (B,), cur), _ints(_need(held, "held"), "held", (B,), cur),
+        _ints(_need(free_count, "free_count"), "free_count", (1,), cur), _ints(block_table, "block_table", (B, max_pages), cur),
+        _ints(free_list, "free_list", free_list.shape, cur), _ints(lens_out, "lens_out", (B,), cur),
+        _ints(held_out, "held_out", (B,), cur), _ints(free_count_out, "free_count_out", (1,), cur),
+        _ints(slot_map, "slot_map", (n_rows,), cur), _ints(row_start, "row_start", (B + 1,), cur),
+        _ints(status, "status", (B,), cur), B, max_pages, int(page_size), int(num_pages), free_list.shape[0], int(n_rows),
+        raw if stream is None else stream.cuda_stream), lib)
     return BlockTables(lens_out, held_out, free_count_out, slot_map, row_start, status)
 
 
-def _rows(t, name, like, N):
+def _rows(t, name, like, N, dev):
     """Pointer and (token, head) strides of a [N, Hkv, d] tensor whose rows are contiguous."""
-    import torch
     _, Hkv, _, d = like.shape
-    if tuple(t.shape) != (N, Hkv, d) or t.dtype != like.dtype:
+    if t.shape != (N, Hkv, d) or t.dtype is not like.dtype:
         raise ValueError(f"{name} must be [N, Hkv, d] = {(N, Hkv, d)} with the cache's dtype (got {tuple(t.shape)}, {t.dtype})")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device} but the library runs on the current device "
-                         f"cuda:{torch.cuda.current_device()} (select it with torch.cuda.device)")
-    if t.stride(2) != 1 and N > 0:
+    if t.get_device() != dev:
+        _dev(t, name)
+    token, head, last = t.stride()
+    if last != 1 and N > 0:
         raise ValueError(f"{name} must have contiguous rows (stride 1 in d)")
     # the stride of a dimension of size one is arbitrary and unused
-    return t.data_ptr(), t.stride(0) if N > 1 else 0, t.stride(1) if Hkv > 1 else 0
+    return t.data_ptr(), token if N > 1 else 0, head if Hkv > 1 else 0
 
 
 def cache_append(k, v, slot_map, kcache, vcache, stream=None):
@@ -489,11 +512,13 @@ def cache_append(k, v, slot_map, kcache, vcache, stream=None):
     num_pages, Hkv, page_size, d = _caches(kcache, vcache)
     N = k.shape[0]
     lib = load_library()
-    kp, kt, kh = _rows(k, "k", kcache, N)
-    vp, vt, vh = _rows(v, "v", kcache, N)
-    _check(lib.jetlong_cache_append(kp, vp, _ints(slot_map, "slot_map", (N,)), _dev(kcache, "kcache"),
-                                    _dev(vcache, "vcache"), N, Hkv, d, kt, kh, vt, vh, num_pages, page_size,
-                                    _dtype_code(kcache), _stream(stream)), lib)
+    cur, raw = _current()
+    kp, kt, kh = _rows(k, "k", kcache, N, cur)
+    vp, vt, vh = _rows(v, "v", kcache, N, cur)
+    _check(lib.jetlong_cache_append(kp, vp, _ints(_need(slot_map, "slot_map"), "slot_map", (N,), cur),
+                                    _ptr(kcache, "kcache", cur), _ptr(vcache, "vcache", cur), N, Hkv, d, kt, kh, vt, vh,
+                                    num_pages, page_size, _dtype_code(kcache),
+                                    raw if stream is None else stream.cuda_stream), lib)
 
 
 def decode_tree_workspace_size(B: int, Hq: int, Hkv: int, d: int, max_nodes: int = 1) -> int:
@@ -540,13 +565,14 @@ def decode_tree(q, kcache, vcache, block_table, lens, row_start, parents=None, o
         workspace = torch.empty(decode_tree_workspace_size(B, Hq, Hkv, d, int(max_nodes)), dtype=torch.uint8,
                                 device=q.device)
     scale = 1.0 / math.sqrt(d) if scale is None else scale
+    cur, raw = _current()
     _check(lib.jetlong_decode_tree(
-        _dev(q, "q"), _dev(kcache, "kcache"), _dev(vcache, "vcache"), _dev(out, "out"),
-        _ints(block_table, "block_table", (B, max_pages)), _ints(lens, "lens", (B,)),
-        _ints(row_start, "row_start", (B + 1,), True), _ints(parents, "parents", (N,), True), B, N, Hq, Hkv, d,
-        num_pages, page_size, max_pages, int(max_nodes), int(w0), int(w_pretrained), float(rope_theta), float(scale),
-        _dtype_code(q), _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream(stream)), lib)
+        _ptr(q, "q", cur), _ptr(kcache, "kcache", cur), _ptr(vcache, "vcache", cur), _ptr(out, "out", cur),
+        _ints(block_table, "block_table", (B, max_pages), cur), _ints(_need(lens, "lens"), "lens", (B,), cur),
+        _ints(row_start, "row_start", (B + 1,), cur), _ints(parents, "parents", (N,), cur), B, N, Hq, Hkv, d, num_pages,
+        page_size, max_pages, int(max_nodes), int(w0), int(w_pretrained), float(rope_theta), float(scale), _dtype_code(q),
+        _ptr(workspace, "workspace", cur), workspace.numel() * workspace.element_size(),
+        raw if stream is None else stream.cuda_stream), lib)
     return out
 
 
@@ -565,11 +591,13 @@ def tree_commit(kcache, vcache, block_table, lens, row_start, parents, last, *, 
     # without parents (chains) the token rows are not read and need no bound
     N = 2147483647 if parents is None else parents.numel()
     lib = load_library()
+    cur, raw = _current()
     _check(lib.jetlong_tree_commit(
-        _dev(kcache, "kcache"), _dev(vcache, "vcache"), _ints(block_table, "block_table", (B, max_pages)),
-        _ints(lens, "lens", (B,)), _ints(row_start, "row_start", (B + 1,)), _ints(parents, "parents", (N,), True),
-        _ints(last, "last", (B,)), _ints(lens_out, "lens_out", (B,)), _ints(n_accepted, "n_accepted", (B,)), B, N,
-        Hkv, d, num_pages, page_size, max_pages, int(max_nodes), _dtype_code(kcache), _stream(stream)), lib)
+        _ptr(kcache, "kcache", cur), _ptr(vcache, "vcache", cur), _ints(block_table, "block_table", (B, max_pages), cur),
+        _ints(lens, "lens", (B,), cur), _ints(_need(row_start, "row_start"), "row_start", (B + 1,), cur),
+        _ints(parents, "parents", (N,), cur), _ints(_need(last, "last"), "last", (B,), cur),
+        _ints(lens_out, "lens_out", (B,), cur), _ints(n_accepted, "n_accepted", (B,), cur), B, N, Hkv, d, num_pages,
+        page_size, max_pages, int(max_nodes), _dtype_code(kcache), raw if stream is None else stream.cuda_stream), lib)
     return lens_out, n_accepted
 
 

@@ -406,13 +406,19 @@ template <typename T, int D, int RT>
 cudaError_t run_simt(const PagedProblem& p, cudaStream_t st, int* nlaunch)
 {
     constexpr int smem = SimtCfg<D, RT>::END;
-    cudaError_t e = cudaFuncSetAttribute(decode_paged_simt_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static PerDevice once;
+    int slots = 0;  // CTAs the device holds at a time
+    cudaError_t e = once.get(&slots, [](int* n, int dev) {
+        int nsm = 0, occ = 0;
+        cudaError_t err = cudaFuncSetAttribute(decode_paged_simt_kernel<T, D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (err == cudaSuccess) err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+        if (err == cudaSuccess)
+            err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_paged_simt_kernel<T, D, RT>, PS_NT, smem);
+        *n = nsm * std::max(1, occ);
+        return err;
+    });
     if (e != cudaSuccess) return e;
-    int dev = 0, nsm = 148, occ = 1;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_paged_simt_kernel<T, D, RT>, PS_NT, smem);
-    const int grid = std::min(kSimtCtas, nsm * std::max(1, occ));
+    const int grid = std::min(kSimtCtas, slots);
     decode_paged_simt_kernel<T, D, RT><<<grid, PS_NT, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *nlaunch += 1;

@@ -58,10 +58,9 @@ __global__ void __launch_bounds__(512, 1)
     using C = RowCfg<D, NROWS>;
     constexpr bool PAIR = NROWS == 256;
     constexpr int NSK = C::NSK, NSV = C::NSV;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const Role<C> ro(p, ln, smem);
-    const Bars<C>& bars = ro.bars;
+    unsigned char* const smem = smem_base();
+    const Role<C> ro(p, ln);
+    const Bars<C> bars;
     uint64_t *sfull = bars.extra, *pfull = sfull + 2, *pvdone = pfull + 4;  // per stream; pfull per half of the keys
     const int warp = ro.warp, lane = ro.lane;
     const uint32_t tmem = start_cta<C, 512>(ro, [&] {
@@ -423,10 +422,13 @@ cudaError_t run_one(const PagedProblem& p, const Launch& ln, cudaStream_t st, in
     if ((e = tc::make_map(&tv, p.vc, D, p.page_size, p.page_size, planes, box)) != cudaSuccess) return e;
     constexpr int smem = RowCfg<D, NROWS>::TOTAL;
     auto kern = decode_paged_rows_kernel<D, NROWS>;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    int dev = 0, nsm = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    static PerDevice once;
+    int nsm = 0;
+    e = once.get(&nsm, [&](int* n, int dev) {
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return err == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : err;
+    });
+    if (e != cudaSuccess) return e;
     *grid = std::min(nsm, kTcCtas);
     kern<<<*grid, 512, smem, st>>>(tk, tv, p, ln);
     return cudaGetLastError();

@@ -86,11 +86,9 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
 {
     using C = Cfg<D, NCOL>;
     constexpr int NSK = C::NSK, NSV = C::NSV;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    // 1024-byte aligned by an offset, not by a cast: the compiler keeps seeing shared memory
-    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const Role<C> ro(p, ln, smem);
-    const Bars<C>& bars = ro.bars;
+    unsigned char* const smem = smem_base();
+    const Role<C> ro(p, ln);
+    const Bars<C> bars;
     uint64_t *sfull = bars.extra, *pfull = sfull + 2, *pvdone = pfull + 2;
     const int warp = ro.warp, lane = ro.lane;
     constexpr uint32_t TCOLS = 256, TS = C::NPV;  // S at 0 and TS, O at 2 TS
@@ -464,10 +462,13 @@ cudaError_t run(const PagedProblem& p, const Launch& ln, cudaStream_t st, int* g
     if ((e = tc::make_map(&tv, p.vc, D, p.page_size, p.page_size, planes, box)) != cudaSuccess) return e;
     constexpr int smem = Cfg<D, NCOL>::TOTAL;
     auto kern = decode_paged_tc_kernel<D, NCOL>;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    int dev = 0, nsm = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    static PerDevice once;
+    int nsm = 0;
+    e = once.get(&nsm, [&](int* n, int dev) {
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return err == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : err;
+    });
+    if (e != cudaSuccess) return e;
     *grid = std::min(nsm, kTcCtas);
     kern<<<*grid, Cfg<D, NCOL>::THREADS, smem, st>>>(tk, tv, p, ln);
     return cudaGetLastError();

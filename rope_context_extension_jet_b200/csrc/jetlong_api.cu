@@ -808,6 +808,21 @@ static int check_pages(int num_pages, int page_size, int max_pages, int* shift)
     return JETLONG_OK;
 }
 
+// Phase constants of the last (d, theta) this host thread used in a paged decode:
+// computing them takes longer than a launch, and a program keeps its theta.
+static const jl::RopeTurns& cached_turns(int d, double rope_theta)
+{
+    thread_local jl::RopeTurns turns;
+    thread_local int cached_d = 0;
+    thread_local double cached_theta = 0.0;
+    if (cached_d != d || cached_theta != rope_theta) {
+        jl::make_rope_turns(&turns, d, rope_theta);
+        cached_d = d;
+        cached_theta = rope_theta;
+    }
+    return turns;
+}
+
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int jetlong_block_tables(const int32_t* lens, const int32_t* grow, const int32_t* release, const int32_t* held,
@@ -969,7 +984,7 @@ int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, v
     p.num_pages = num_pages; p.page_size = page_size; p.max_pages = max_pages; p.max_nodes = max_nodes;
     p.w0 = w0; p.w_pre = w_pretrained;
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    jl::make_rope_turns(&p.turns, d, rope_theta);
+    p.turns = cached_turns(d, rope_theta);
     p.workspace = static_cast<unsigned char*>(workspace);
     take_injection(&p.inject, &p.wait_cycles);
     int n = 0;

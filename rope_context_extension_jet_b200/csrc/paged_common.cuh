@@ -9,6 +9,8 @@
 // the device input word that jetlong_device_status reports.
 #pragma once
 
+#include <mutex>
+
 #include "jl_common.cuh"
 
 namespace jl {
@@ -66,6 +68,29 @@ struct CommitProblem {
     int *lens_out, *n_accepted;
     int B, N, Hkv, row_bytes, num_pages, page_size, page_shift, max_pages, max_nodes;
     int* input_error;
+};
+
+// Per device, done once: `set` (a kernel's attributes, its occupancy) and the number it
+// returns through *value.  Such calls cost as much as a launch.
+struct PerDevice {
+    std::mutex mu;
+    bool known[64] = {};
+    int value[64] = {};
+    template <class F>
+    cudaError_t get(int* out, F set)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lk(mu);
+        if (!known[dev]) {
+            if ((e = set(&value[dev], dev)) != cudaSuccess) return e;
+            known[dev] = true;
+        }
+        *out = value[dev];
+        return cudaSuccess;
+    }
 };
 
 cudaError_t launch_block_tables(const TablesProblem& p, cudaStream_t s, int* nlaunch);

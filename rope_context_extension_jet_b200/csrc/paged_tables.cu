@@ -197,8 +197,12 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
 cudaError_t launch_block_tables(const TablesProblem& p, cudaStream_t s, int* nlaunch)
 {
     const int smem = 5 * (p.B + 1) * (int)sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         5 * (kMaxTableRequests + 1) * (int)sizeof(int));
+    static PerDevice once;
+    int unused = 0;
+    cudaError_t e = once.get(&unused, [](int*, int) {
+        return cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    5 * (kMaxTableRequests + 1) * (int)sizeof(int));
+    });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at{};

@@ -73,6 +73,15 @@ struct Notes {
     static_assert(INFO > NSK + 1, "ring of per-item notes");
 };
 
+// The CTA's dynamic shared memory from its first 1024-byte boundary on.  Derived from
+// the array by an offset, not by a cast through an integer, so that the compiler
+// keeps seeing shared memory.
+__device__ __forceinline__ unsigned char* smem_base()
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    return smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+}
+
 // The barriers, in the order of their use.
 template <class C>
 struct Bars {
@@ -82,9 +91,9 @@ struct Bars {
     uint64_t *qready;                   // queries of a phase rotated
     uint64_t *dfull, *dfree;            // unit planned; done with
     uint64_t *drain, *extra;
-    __device__ __forceinline__ explicit Bars(unsigned char* smem)
+    __device__ __forceinline__ Bars()
     {
-        kfull = reinterpret_cast<uint64_t*>(smem + C::BAR);
+        kfull = reinterpret_cast<uint64_t*>(smem_base() + C::BAR);
         kready = kfull + C::NSK;
         kempty = kready + C::NSK;
         vfull = kempty + C::NSK;
@@ -169,38 +178,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r)
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// Bounded wait of a whole warp on a barrier phase, as tc::warp_wait, but the
-// hardware may park the warp for up to kParkNs per try: polling warps would take
-// issue slots from the ones at work (the largest trees ran at half their speed).
-constexpr uint32_t kParkNs = 100000;
-__device__ __forceinline__ bool try_wait_parked(uint64_t* bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(kParkNs) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* dev_error, long long limit,
-                                          int code)
-{
-    bool ok = try_wait_parked(bar, parity);
-    if (!ok) {
-        const long long t0 = clock64();
-        while (!(ok = try_wait_parked(bar, parity))) {
-            if (*abort_flag) break;
-            if (clock64() - t0 > limit) {
-                record_error(dev_error, code);
-                *abort_flag = 1;
-                break;
-            }
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
 {
     asm volatile(
@@ -234,30 +211,26 @@ template <class C>
 struct Role {
     const PagedProblem& p;
     const Launch& ln;
-    unsigned char* smem;
-    Bars<C> bars;
-    volatile int* abort_flag;
     int warp, lane;
-    __device__ __forceinline__ Role(const PagedProblem& p_, const Launch& ln_, unsigned char* smem_)
-        : p(p_), ln(ln_), smem(smem_), bars(smem_)
+    __device__ __forceinline__ Role(const PagedProblem& p_, const Launch& ln_) : p(p_), ln(ln_)
     {
-        abort_flag = reinterpret_cast<volatile int*>(smem + C::SLOT + 4);
         warp = threadIdx.x >> 5;
         lane = threadIdx.x & 31;
     }
+    __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(smem_base() + C::SLOT + 4); }
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int code) const
     {
-        return warp_wait(bar, parity, abort_flag, ln.dev_error, ln.wait_cycles, code);
+        return tc::warp_wait(bar, parity, abort_flag(), ln.dev_error, ln.wait_cycles, code);
     }
     // unit k of the piece: wait until it is planned; afterwards each warp hands it back
-    __device__ __forceinline__ bool unit_wait(int k, int code) const { return wait(&bars.dfull[k % UNITS], (k / UNITS) & 1, code); }
-    __device__ __forceinline__ UnitPtr unit(int k) const { return reinterpret_cast<UnitDesc*>(smem + C::DESC) + k % UNITS; }
+    __device__ __forceinline__ bool unit_wait(int k, int code) const { return wait(&Bars<C>().dfull[k % UNITS], (k / UNITS) & 1, code); }
+    __device__ __forceinline__ UnitPtr unit(int k) const { return reinterpret_cast<UnitDesc*>(smem_base() + C::DESC) + k % UNITS; }
     __device__ __forceinline__ void unit_done(int k) const
     {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.dfree[k % UNITS]);
+        if (lane == 0) mbar_arrive(&Bars<C>().dfree[k % UNITS]);
     }
-    __device__ __forceinline__ volatile unsigned* note() const { return reinterpret_cast<volatile unsigned*>(smem + C::NOTE); }
+    __device__ __forceinline__ volatile unsigned* note() const { return reinterpret_cast<volatile unsigned*>(smem_base() + C::NOTE); }
     __device__ __forceinline__ unsigned all_pages() const { return (1u << (KT >> min(p.page_shift, 7))) - 1; }
 };
 
@@ -266,25 +239,25 @@ struct Role {
 template <class C, uint32_t TCOLS, class InitExtra>
 __device__ __forceinline__ uint32_t start_cta(const Role<C>& ro, InitExtra init_extra)
 {
-    uint32_t* slot = reinterpret_cast<uint32_t*>(ro.smem + C::SLOT);
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem_base() + C::SLOT);
     const int tid = threadIdx.x;
     if (tid == 0) {
-        Bars<C> bars(ro.smem);
+        Bars<C> bars;
         bars.init();
         init_extra();
-        *ro.abort_flag = *reinterpret_cast<volatile int*>(ro.ln.dev_error) != 0;  // an earlier wait ran out: no work
+        *ro.abort_flag() = *reinterpret_cast<volatile int*>(ro.ln.dev_error) != 0;  // an earlier wait ran out: no work
         fence_mbar_init();
     }
     for (int m = tid; m < C::DIM / 2; m += C::THREADS)
-        reinterpret_cast<uint2*>(ro.smem + C::TURNS)[m] = make_uint2(ro.p.turns.hi[m], ro.p.turns.lo[m]);
+        reinterpret_cast<uint2*>(smem_base() + C::TURNS)[m] = make_uint2(ro.p.turns.hi[m], ro.p.turns.lo[m]);
     if (ro.warp == 2) {
         tmem_alloc(slot, TCOLS);
         tmem_relinquish();
         tc_fence_before();
     }
     // ends with a barrier of the CTA
-    piece_plan<KT, C::ROWS, C::THREADS>(ro.p, ro.ln.min_items, reinterpret_cast<PiecePlan*>(ro.smem + C::PLAN),
-                                        reinterpret_cast<long long*>(ro.smem + C::SCAN));
+    piece_plan<KT, C::ROWS, C::THREADS>(ro.p, ro.ln.min_items, reinterpret_cast<PiecePlan*>(smem_base() + C::PLAN),
+                                        reinterpret_cast<long long*>(smem_base() + C::SCAN));
     tc_fence_after();
     return *slot;
 }
@@ -296,12 +269,13 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
 {
     const PagedProblem& p = ro.p;
     const Launch& ln = ro.ln;
-    unsigned char* smem = ro.smem;
+    unsigned char* const smem = smem_base();
+    const Bars<C> bars;
     const int lane = ro.lane;
     constexpr int D = C::DIM;
         constexpr int NS = isK ? C::NSK : C::NSV;
-    uint64_t* full = isK ? ro.bars.kfull : ro.bars.vfull;
-    uint64_t* empty = isK ? ro.bars.kempty : ro.bars.vempty;
+    uint64_t* full = isK ? bars.kfull : bars.vfull;
+    uint64_t* empty = isK ? bars.kempty : bars.vempty;
         unsigned char* ring = smem + (isK ? C::K0 : C::V0);
     const int box = min(p.page_size, KT);
     int e = 0;
@@ -357,11 +331,12 @@ template <class C>
 __device__ __forceinline__ void plan_units(const Role<C>& ro)
 {
     const PagedProblem& p = ro.p;
-    const PiecePlan* plan = reinterpret_cast<const PiecePlan*>(ro.smem + C::PLAN);
+    const PiecePlan* plan = reinterpret_cast<const PiecePlan*>(smem_base() + C::PLAN);
+    const Bars<C> bars;
     if (ro.lane == 0) {
         clear_cut(p);
         long long cur = plan->start, base = plan->base;
-        const long long end = *ro.abort_flag ? cur : plan->end;
+        const long long end = *ro.abort_flag() ? cur : plan->end;
         int b = plan->b, k = 0;
         for (;; ++k) {
             UnitDesc u;
@@ -394,10 +369,10 @@ __device__ __forceinline__ void plan_units(const Role<C>& ro)
                 if (u.i0 == 0 && u.i1 < s.items) note_cut(p, s, plan->per, cur, u.kvh, u.r0, u.rows);
                 cur += u.i1 - u.i0;
             }
-            if (k >= UNITS && !tc::wait_or_abort(&ro.bars.dfree[k % UNITS], ((k / UNITS) - 1) & 1, ro.abort_flag, ro.ln.dev_error, ro.ln.wait_cycles, 0x441))
+            if (k >= UNITS && !tc::wait_or_abort(&bars.dfree[k % UNITS], ((k / UNITS) - 1) & 1, ro.abort_flag(), ro.ln.dev_error, ro.ln.wait_cycles, 0x441))
                 break;
-            reinterpret_cast<UnitDesc*>(ro.smem + C::DESC)[k % UNITS] = u;
-            mbar_arrive(&ro.bars.dfull[k % UNITS]);
+            reinterpret_cast<UnitDesc*>(smem_base() + C::DESC)[k % UNITS] = u;
+            mbar_arrive(&bars.dfull[k % UNITS]);
             if (u.rows == 0) break;
         }
     }
@@ -412,7 +387,8 @@ template <class C>
 __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
 {
     const PagedProblem& p = ro.p;
-    unsigned char* smem = ro.smem;
+    unsigned char* const smem = smem_base();
+    const Bars<C> bars;
     const int lane = ro.lane;
     constexpr int D = C::DIM, H = D / 2, CH = D / 16, NSK = C::NSK, NSV = C::NSV;
     float* ksc = reinterpret_cast<float*>(smem + C::KSC);
@@ -480,8 +456,8 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
         int* big = reinterpret_cast<int*>(bad + 1);
         // the softmax is done with unit nu - 2, the tensor cores with the
         // queries of unit nu - 1
-        ok = ok && (nu < 2 || ro.wait(&ro.bars.ufree[nu & 1], ((nu >> 1) - 1) & 1, 0x421)) &&
-             (e == 0 || ro.wait(&ro.bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x422));
+        ok = ok && (nu < 2 || ro.wait(&bars.ufree[nu & 1], ((nu >> 1) - 1) & 1, 0x421)) &&
+             (e == 0 || ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x422));
         if ((agreed = named_or(1, C::ROTALL, !ok))) break;
         const int L = ud->L, T = ud->T, n = L + T, rows = ud->rows, r0 = ud->r0, kvh = ud->kvh;
         if (t < T) {
@@ -547,7 +523,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             qsc[row] = sc;
         }
         named_sync(1, C::ROTALL);
-        if (lane == 0) mbar_arrive(&ro.bars.uready[nu & 1]);
+        if (lane == 0) mbar_arrive(&bars.uready[nu & 1]);
         const bool always = *big != 0;
         int gcur = -1;
         uint32_t dm = 0, ds1 = 0, ds2 = 0;  // division by the group size by multiply-shift
@@ -555,7 +531,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             const int g = it.g;
             if (g != gcur) {
                 // queries of this phase; the tensor cores are done with those of the last
-                if (gcur >= 0 && !ro.wait(&ro.bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423)) { ok = false; break; }
+                if (gcur >= 0 && !ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423)) { ok = false; break; }
                 gcur = g;
                 const uint32_t dv = max(g, 1);
                 const uint32_t lg = 32 - __clz(dv - 1);  // ceil(log2 dv); 0 for 1
@@ -587,7 +563,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ro.bars.qready);
+                if (lane == 0) mbar_arrive(bars.qready);
             }
             if (C::ALT && (e & 1) != group) continue;
             const int st = e % NSK, j0 = it.tile * KT;
@@ -606,7 +582,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             float2 cs[4], sn[4];
             angles(f, cs, sn);
             unsigned scaled = 0;
-            if (!ro.wait(&ro.bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
+            if (!ro.wait(&bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
             // from row to row the turned position stays or steps by one (drafted
             // rows may jump): the angles follow by the angle addition
             auto advance = [&](int r) {
@@ -667,7 +643,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             if (lane == 0) reinterpret_cast<volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 4 + (rt >> 5)] = scaled;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ro.bars.kready[st]);
+            if (lane == 0) mbar_arrive(&bars.kready[st]);
             // value rows that do not exist count as zero: the page may hold
             // anything there, and a weight of 0 does not silence NaN.  A drafted
             // row's own infinities and NaN are cleared as well (nodes beside it
@@ -675,7 +651,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             const unsigned have = ro.note()[e % INFO];
             if (drafted || have != all_pages) {
                 const int sv = e % NSV;
-                if (!ro.wait(&ro.bars.vfull[sv], (e / NSV) & 1, 0x425)) { ok = false; break; }
+                if (!ro.wait(&bars.vfull[sv], (e / NSV) & 1, 0x425)) { ok = false; break; }
                 unsigned char* vt = smem + C::V0 + sv * C::TILE;
                 constexpr int TPR = C::ROT / KT;  // threads per row
                 const int r = rt / TPR, j = j0 + r;
@@ -704,7 +680,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ro.bars.vfix[sv]);
+                if (lane == 0) mbar_arrive(&bars.vfix[sv]);
             }
         }
         ro.unit_done(nu);
