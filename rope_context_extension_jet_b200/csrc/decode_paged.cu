@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
 
     piece_plan<PS_KT, RT, PS_NT>(p, 2, plan, reinterpret_cast<long long*>(plan + 1));
     if (tid == 0) clear_cut(p);
+    let_merge_start();
     long long cur = plan->start, base = plan->base;
     const long long end = plan->end;
     int b = plan->b;

@@ -24,6 +24,7 @@
 
 namespace jl {
 namespace ptc {
+namespace {
 
 template <int D, int NROWS>
 struct RowTiles {
@@ -46,7 +47,7 @@ struct RowCfg : RowTiles<D, NROWS>,
     // Registers per thread after setmaxnreg: producers / issuer / planner, rotation,
     // each softmax warpgroup.  An increase draws on what the block was launched with
     // (512 x 128).
-    static constexpr int R_PROD = 56, R_ROT = 96, R_SOFT = 176;
+    static constexpr int R_PROD = 56, R_ROT = 104, R_SOFT = 176;
     static_assert((R_PROD + R_ROT + 2 * R_SOFT) * 128 <= 512 * 128, "register split");
 };
 
@@ -433,6 +434,8 @@ cudaError_t run_one(const PagedProblem& p, const Launch& ln, cudaStream_t st, in
     kern<<<*grid, 512, smem, st>>>(tk, tv, p, ln);
     return cudaGetLastError();
 }
+
+}  // namespace
 
 cudaError_t run_rows(const PagedProblem& p, int d, int rows, const Launch& ln, cudaStream_t st, int* grid)
 {

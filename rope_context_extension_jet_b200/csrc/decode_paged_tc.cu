@@ -32,6 +32,7 @@
 
 namespace jl {
 namespace ptc {
+namespace {
 
 template <int D, int NCOL>
 struct CfgTiles {
@@ -55,8 +56,8 @@ template <int D, int NCOL>
 struct Cfg : CfgTiles<D, NCOL>,
              Notes<D, NCOL, CfgTiles<D, NCOL>::NSK, CfgTiles<D, NCOL>::NSV, CfgTiles<D, NCOL>::BASE, 6, 16> {
     static constexpr int M0 = Cfg::NOTES_END;               // [NCOL] minus the column references, [NCOL] zeros
-    static constexpr int RED = M0 + NCOL * 8;               // [4][NCOL] column maxima / sums
-    static constexpr int TOTAL = RED + 4 * NCOL * 4 + 1024;
+    static constexpr int RED = M0 + NCOL * 8;               // [4][NCOL] column maxima / sums, [NCOL] rescale factors
+    static constexpr int TOTAL = RED + 5 * NCOL * 4 + 1024;
     static_assert(TOTAL <= 232448, "shared memory");
 };
 
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
         float* nref = reinterpret_cast<float*>(smem + C::M0);
         float* zero = nref + NCOL;
         float* red = reinterpret_cast<float*>(smem + C::RED);
+        float* alpha = red + 4 * NCOL;
         float l[NCOL];  // sums over this thread's keys
         int e = 0, nu = 0;
         // as above, a wait that ran out is carried to the warpgroup's next barrier,
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                     }
                 };
                 float y[NCOL];
-                for (bool rel = true;; rel = !rel) {
+                for (bool rel = !first;; rel = !rel) {  // the first tile sets its references first
                     float top = -INFINITY;
                     {
                         logits(y, rel ? nref : zero);
@@ -321,20 +323,20 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                     }
                     // sums and O follow the new references
                     named_sync(bid, 128);
-                    float alpha = 1.f;
                     if (key < NCOL && key < (cols + 15) / 16 * 16) {
                         const float m = fmaxf(fmaxf(red[key], red[NCOL + key]), fmaxf(red[2 * NCOL + key], red[3 * NCOL + key]));
                         const float old = -nref[key];
+                        float a = 1.f;
                         if (m > -INFINITY && m + kAbove > old) {
                             nref[key] = -(m + kAbove);
-                            alpha = exp2f(old - (m + kAbove));
+                            a = exp2f(old - (m + kAbove));
                         }
+                        alpha[key] = a;
                     }
                     named_sync(bid, 128);
-                    if (key < NCOL) red[key] = alpha;
-                    named_sync(bid, 128);
 #pragma unroll
-                    for (int c = 0; c < NCOL; ++c) l[c] *= red[c];
+                    for (int c = 0; c < NCOL; ++c)
+                        if ((c & ~15) < cols) l[c] *= alpha[c];
                     if (!first) {
                         ok = ro.wait(&pvdone[(e - 1) & 1], ((e - 1) >> 1) & 1, 0x433);
                         tc_fence_after();
@@ -345,12 +347,12 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                             tmem_ld16(tl + 2 * TS + c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * red[c + x]);
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha[c + x]);
                             tmem_st16(tl + 2 * TS + c, o);
                         }
                         tmem_wait_st();
                     }
-                    if (named_or(bid, 128, !ok)) {  // and red is read before it is written again
+                    if (named_or(bid, 128, !ok)) {  // and alpha is read before it is written again
                         stop = true;
                         break;
                     }
@@ -403,6 +405,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(un + C::U_BAD);
             float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
                           ((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NCOL * (D + 2);
+            int node = r0 / p.group, hd = r0 % p.group;
 #pragma unroll 1
             for (int cb = 0; cb < NCOL; cb += 16) {
                 if (cb >= cols) break;
@@ -416,6 +419,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                     float val = __uint_as_float(o[x]);
                     const float sum = red[c] + red[NCOL + c] + red[2 * NCOL + c] + red[3 * NCOL + c];
                     if (bad && key < D) {
+                        asm volatile("" ::: "memory");
                         // infinities and NaN of drafted rows this node attends
                         for (unsigned long long rest = bad & canc[c]; rest; rest &= rest - 1) {
                             const int row = L + __ffsll((long long)rest) - 1;
@@ -425,15 +429,18 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                             if (!(fabsf(v) < INFINITY)) val += v;
                         }
                     }
-                    const int r = c;
-                    if (whole) {
-                        const int node = (r0 + r) / p.group, hd = kvh * p.group + (r0 + r) % p.group;
-                        if (key < D)
-                            static_cast<__nv_bfloat16*>(p.out)[((size_t)(n0 + node) * p.Hq + hd) * D + key] =
-                                __float2bfloat16_rn(val / sum);
-                    } else {
-                        if (key < D) part[(size_t)r * (D + 2) + key] = val;
-                        if (key < 2) part[(size_t)r * (D + 2) + D + key] = key == 0 ? (nref[c] == -kNoRef ? -INFINITY : -nref[c]) : sum;
+                    if (key < D) {
+                        if (whole)
+                            static_cast<__nv_bfloat16*>(p.out)[((size_t)(n0 + node) * p.Hq + kvh * p.group + hd) * D + key] =
+                                __float2bfloat16_rn(__fdividef(val, sum));
+                        else
+                            part[(size_t)c * (D + 2) + key] = val;
+                    }
+                    if (!whole && key < 2)
+                        part[(size_t)c * (D + 2) + D + key] = key == 0 ? (nref[c] == -kNoRef ? -INFINITY : -nref[c]) : sum;
+                    if (++hd == p.group) {
+                        hd = 0;
+                        ++node;
                     }
                 }
             }
@@ -473,6 +480,8 @@ cudaError_t run(const PagedProblem& p, const Launch& ln, cudaStream_t st, int* g
     kern<<<*grid, Cfg<D, NCOL>::THREADS, smem, st>>>(tk, tv, p, ln);
     return cudaGetLastError();
 }
+
+}  // namespace
 
 cudaError_t run_cols(const PagedProblem& p, int d, int cols, const Launch& ln, cudaStream_t st, int* grid)
 {

@@ -102,6 +102,10 @@ size_t paged_tc_workspace(int rows, int d);
 cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s, int* grid);
 cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch);
 
+// Lets the merge kernel's CTAs start where there is room; they wait on the device
+// for the end of this grid.
+__device__ __forceinline__ void let_merge_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void record_input(int* word, int code)
 {
     if (word) atomicCAS(word, 0, code);
@@ -225,6 +229,7 @@ constexpr size_t kPagedHeader = 512 * sizeof(CutUnit);
 struct PiecePlan {
     long long start, end, base, per;
     int b;
+    SeqPlan first;  // plan of request b
 };
 
 template <int KT, int RT, int NTHR>
@@ -268,6 +273,7 @@ __device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out,
             if (at <= start && start < at + c) {
                 out->b = b;
                 out->base = at;
+                out->first = s;
             }
             at += c;
         }

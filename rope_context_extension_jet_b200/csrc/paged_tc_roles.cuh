@@ -57,8 +57,8 @@ struct Notes {
     static constexpr int UNIT = BASE;
     static constexpr int U_ANC = 0, U_DEPTH = U_ANC + ROWS * 8, U_LIM = U_DEPTH + kMaxNodes * 4, U_QG = U_LIM + ROWS * 4;
     static constexpr int U_CQ = U_QG + ROWS * 4, U_BAD = U_CQ + ROWS * 4, UBYTES = U_BAD + 16;
-    static constexpr int QS = UNIT + 2 * UBYTES;            // [ROWS] query scales, [ROWS] positions
-    static constexpr int PAR = QS + ROWS * 8;               // [64] parents, [64] node ancestors
+    static constexpr int QS = UNIT + 2 * UBYTES;            // [ROWS] query scales
+    static constexpr int PAR = QS + ROWS * 4;               // [64] parents, [64] node ancestors
     static constexpr int KSC = PAR + kMaxNodes * 12;        // [INFO][128] inverse key scales
     static constexpr int TURNS = KSC + INFO * KT * 4;       // [D / 2] phase constants (hi, lo)
     static constexpr int NOTE = TURNS + D / 2 * 8;          // [INFO] mask of the pages present
@@ -259,6 +259,7 @@ __device__ __forceinline__ uint32_t start_cta(const Role<C>& ro, InitExtra init_
     piece_plan<KT, C::ROWS, C::THREADS>(ro.p, ro.ln.min_items, reinterpret_cast<PiecePlan*>(smem_base() + C::PLAN),
                                         reinterpret_cast<long long*>(smem_base() + C::SCAN));
     tc_fence_after();
+    let_merge_start();
     return *slot;
 }
 
@@ -338,11 +339,11 @@ __device__ __forceinline__ void plan_units(const Role<C>& ro)
         long long cur = plan->start, base = plan->base;
         const long long end = *ro.abort_flag() ? cur : plan->end;
         int b = plan->b, k = 0;
+        SeqPlan s = plan->first;
         for (;; ++k) {
             UnitDesc u;
             u.rows = 0;
             if (cur < end) {
-                SeqPlan s = seq_plan<KT, C::ROWS>(p, b, false);
                 long long cnt = (long long)s.items * s.row_tiles * p.Hkv;
                 while (cur >= base + cnt) {
                     base += cnt;
@@ -398,18 +399,29 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
     const int c = t % CH, row0 = (rt / CH) * RPT;
     const uint4* turns = reinterpret_cast<const uint4*>(smem + C::TURNS) + c * 4;  // the thread's 8 frequencies
     float2 stc[4], sts[4];                         // cos, sin of one position step, as frequency pairs
-    auto angles = [&](uint32_t f, float2 (&cs)[4], float2 (&sn)[4]) {
+    struct Angles {
+        float2 cs[4], sn[4];  // cos, sin of the 8 frequencies, as pairs
+    };
+    auto angles = [&](uint32_t f, Angles& a) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const uint4 w2 = turns[u];
-            rope_cs_fast(f, w2.x, w2.y, cs[u].x, sn[u].x);
-            rope_cs_fast(f, w2.z, w2.w, cs[u].y, sn[u].y);
+            rope_cs_fast(f, w2.x, w2.y, a.cs[u].x, a.sn[u].x);
+            rope_cs_fast(f, w2.z, w2.w, a.cs[u].y, a.sn[u].y);
         }
     };
-    angles(1u, stc, sts);
+    {
+        Angles one;
+        angles(1u, one);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            stc[u] = one.cs[u];
+            sts[u] = one.sn[u];
+        }
+    }
     // 8 pairs (lo.x holds dimensions 0, 1 of the chunk, hi.x their partners, ...)
     // turned by (cs, sn), as fp16
-    auto turn = [&](uint4& lo, uint4& hi, const float2 (&cs)[4], const float2 (&sn)[4]) {
+    auto turn = [&](uint4& lo, uint4& hi, const Angles& by) {
         uint32_t* a = &lo.x;
         uint32_t* b = &hi.x;
 #pragma unroll
@@ -417,13 +429,17 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             const float2 x = make_float2(bf16_lo(a[u]), bf16_hi(a[u])), y = make_float2(bf16_lo(b[u]), bf16_hi(b[u]));
             const float2 ny = make_float2(__uint_as_float((b[u] << 16) + 0x80000000u),
                                           __uint_as_float((b[u] & 0xffff0000u) ^ 0x80000000u));
-            const float2 r0 = fma2(ny, sn[u], mul2(x, cs[u])), r1 = fma2(y, cs[u], mul2(x, sn[u]));
+            const float2 r0 = fma2(ny, by.sn[u], mul2(x, by.cs[u])), r1 = fma2(y, by.cs[u], mul2(x, by.sn[u]));
             a[u] = pack_f16x2(r0.x, r0.y);
             b[u] = pack_f16x2(r1.x, r1.y);
         }
     };
     auto absmax8 = [](const uint4& a, const uint4& b) {
         return absmax2(absmax2(absmax2(a.x, a.y), absmax2(a.z, a.w)), absmax2(absmax2(b.x, b.y), absmax2(b.z, b.w)));
+    };
+    auto sum8 = [](const uint4& a) {
+        return fabsf(bf16_lo(a.x)) + fabsf(bf16_hi(a.x)) + fabsf(bf16_lo(a.y)) + fabsf(bf16_hi(a.y)) + fabsf(bf16_lo(a.z)) +
+               fabsf(bf16_hi(a.z)) + fabsf(bf16_lo(a.w)) + fabsf(bf16_hi(a.w));
     };
     auto scale8 = [](uint4& a, float sc) {  // exact: a power of two (elements far below the row's largest may vanish)
         a.x = pack_bf16x2(bf16_lo(a.x) * sc, bf16_hi(a.x) * sc);
@@ -436,7 +452,6 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
     int* par = reinterpret_cast<int*>(smem + C::PAR);
     unsigned long long* nanc = reinterpret_cast<unsigned long long*>(par + kMaxNodes);
     float* qsc = reinterpret_cast<float*>(smem + C::QS);
-    int* qpos = reinterpret_cast<int*>(qsc + C::ROWS);
     int e = 0, nu = 0;
     // A wait that runs out in one warp must not leave the others at a barrier:
     // the warps meet once per unit (and once after the last) and stop together
@@ -459,11 +474,11 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
         ok = ok && (nu < 2 || ro.wait(&bars.ufree[nu & 1], ((nu >> 1) - 1) & 1, 0x421)) &&
              (e == 0 || ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x422));
         if ((agreed = named_or(1, C::ROTALL, !ok))) break;
-        const int L = ud->L, T = ud->T, n = L + T, rows = ud->rows, r0 = ud->r0, kvh = ud->kvh;
+        const int L = ud->L, T = ud->T, n = L + T, rows = ud->rows, r0 = ud->r0, kvh = ud->kvh, n0 = ud->n0;
         if (t < T) {
             int x = t - 1;
             if (p.parents) {
-                x = p.parents[ud->n0 + t];
+                x = p.parents[n0 + t];
                 if (x < -1 || x >= t) {
                     record_input(p.input_error, kBadParent);
                     x = -1;
@@ -486,159 +501,174 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             depth[t] = __popcll(m) - 1;
         }
         named_sync(1, C::ROTALL);
-        for (int row = t; row < C::ROWS; row += C::ROTALL) {
-            int x = 0, G = 0;
-            float inv = 0.f, sc = 0.f;
-            unsigned long long up = 0;
-            if (row < rows) {
-                const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
-                x = L + depth[node];
-                G = x / p.w_pre + 1;
-                up = nanc[node];
-                // the query times a power of two that brings its largest element
-                // into [2^13, 2^14); the logits times the inverse
-                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                ((size_t)(ud->n0 + node) * p.Hq + hd) * D);
-                uint32_t mx = 0;
-                float l1 = 0.f;
-#pragma unroll 4
-                for (int k = 0; k < D / 8; ++k) {
-                    const uint4 v = q[k];
-                    mx = absmax2(mx, absmax2(absmax2(v.x, v.y), absmax2(v.z, v.w)));
-                    l1 += fabsf(bf16_lo(v.x)) + fabsf(bf16_hi(v.x)) + fabsf(bf16_lo(v.y)) + fabsf(bf16_hi(v.y)) +
-                          fabsf(bf16_lo(v.z)) + fabsf(bf16_hi(v.z)) + fabsf(bf16_lo(v.w)) + fabsf(bf16_hi(v.w));
+        // The unit's queries turned for the phase of group size g, as fp16.  CH threads
+        // share a row.  The first time also the row's notes: each query is multiplied by
+        // a power of two that brings its largest element into [2^13, 2^14), its logits
+        // by the inverse.
+        auto queries = [&](int g, bool setup) {
+            const uint32_t dv = max(g, 1);
+#pragma unroll 2
+            for (int x = t; x < C::ROWS * CH; x += C::ROTALL) {
+                const int row = x / CH;  // CH divides the thread count: chunk x % CH = c
+                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                int pos = 0;
+                float sc = 0.f;
+                if (row < rows) {
+                    const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
+                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)(n0 + node) * p.Hq + hd) * D;
+                    lo = *reinterpret_cast<const uint4*>(q + c * 8);
+                    hi = *reinterpret_cast<const uint4*>(q + H + c * 8);
+                    pos = L + depth[node];
                 }
-                const int ex = tc::range_exp(mag16(mx));
-                sc = tc::pow2i(ex);
-                inv = fminf(fmaxf(tc::pow2i(-ex) * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);  // a normal number: -inf times it stays -inf
-                // keys rounded to fp16 as they are err by up to 2^-25 where fp16 is
-                // subnormal; with an L1 norm this large that could reach 2^-11 of a logit
-                if (!(l1 * p.scale_log2 * 1.4142136f <= 16384.f)) *big = 1;
+                if (setup) {
+                    uint32_t mx = mag16(absmax8(lo, hi));
+                    float l1 = sum8(lo) + sum8(hi);
+#pragma unroll
+                    for (int o = 1; o < CH; o <<= 1) {
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+                    }
+                    const int ex = tc::range_exp(mx);
+                    sc = tc::pow2i(ex);
+                    if (c == 0) {
+                        // a normal number: -inf times it stays -inf
+                        const float inv = fminf(fmaxf(tc::pow2i(-ex) * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);
+                        lim0[row] = pos - ud->w0;
+                        qG[row] = row < rows ? pos / p.w_pre + 1 : 0;
+                        canc[row] = row < rows ? nanc[(r0 + row) / p.group] : 0ull;
+                        cq[row] = row < rows ? inv : 0.f;
+                        qsc[row] = sc;
+                        // keys rounded to fp16 as they are err by up to 2^-25 where fp16 is
+                        // subnormal; with an L1 norm this large that could reach 2^-11 of a logit
+                        if (!(l1 * p.scale_log2 * 1.4142136f <= 16384.f)) *big = 1;
+                    }
+                } else {
+                    sc = qsc[row];
+                }
+                Angles by;
+                angles((uint32_t)pos / dv, by);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    by.cs[u] = make_float2(by.cs[u].x * sc, by.cs[u].y * sc);
+                    by.sn[u] = make_float2(by.sn[u].x * sc, by.sn[u].y * sc);
+                }
+                turn(lo, hi, by);
+                *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c)) = lo;
+                *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c + CH)) = hi;
             }
-            qpos[row] = x;
-            lim0[row] = x - ud->w0;
-            qG[row] = G;
-            canc[row] = up;
-            cq[row] = inv;
-            qsc[row] = sc;
-        }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.qready);
+        };
+        UnitItems it(ud);
+        int gcur = it.g;
+        queries(gcur, true);
         named_sync(1, C::ROTALL);
         if (lane == 0) mbar_arrive(&bars.uready[nu & 1]);
         const bool always = *big != 0;
-        int gcur = -1;
         uint32_t dm = 0, ds1 = 0, ds2 = 0;  // division by the group size by multiply-shift
-        for (UnitItems it(ud); it.left > 0; it.next(ud), ++e) {
-            const int g = it.g;
-            if (g != gcur) {
-                // queries of this phase; the tensor cores are done with those of the last
-                if (gcur >= 0 && !ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423)) { ok = false; break; }
-                gcur = g;
-                const uint32_t dv = max(g, 1);
-                const uint32_t lg = 32 - __clz(dv - 1);  // ceil(log2 dv); 0 for 1
-                dm = (uint32_t)(((((uint64_t)1 << 32) * (((uint64_t)1 << lg) - dv)) / dv) + 1);
-                ds1 = min(lg, 1u);
-                ds2 = lg > 1 ? lg - 1 : 0;
-#pragma unroll 1
-                for (int x = t; x < C::ROWS * CH; x += C::ROTALL) {
-                    const int r = x / CH;  // CH divides the thread count: chunk x % CH = c
-                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                    if (r < rows) {
-                        const int node = (r0 + r) / p.group, hd = kvh * p.group + (r0 + r) % p.group;
-                        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                                                 ((size_t)(ud->n0 + node) * p.Hq + hd) * D;
-                        lo = *reinterpret_cast<const uint4*>(q + c * 8);
-                        hi = *reinterpret_cast<const uint4*>(q + H + c * 8);
-                        float2 cs[4], sn[4];
-                        angles((uint32_t)qpos[r] / dv, cs, sn);
-                        const float2 sc = make_float2(qsc[r], qsc[r]);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            cs[u] = mul2(cs[u], sc);
-                            sn[u] = mul2(sn[u], sc);
-                        }
-                        turn(lo, hi, cs, sn);
-                    }
-                    *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(r, c)) = lo;
-                    *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(r, c + CH)) = hi;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.qready);
+        auto set_divisor = [&](int g) {
+            const uint32_t dv = max(g, 1);
+            const uint32_t lg = 32 - __clz(dv - 1);  // ceil(log2 dv); 0 for 1
+            dm = (uint32_t)(((((uint64_t)1 << 32) * (((uint64_t)1 << lg) - dv)) / dv) + 1);
+            ds1 = min(lg, 1u);
+            ds2 = lg > 1 ? lg - 1 : 0;
+        };
+        set_divisor(gcur);
+        for (; it.left > 0; it.next(ud), ++e) {
+            if (it.g != gcur) {
+                // the next phase; the tensor cores are done with the queries of the last
+                if (!ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423)) { ok = false; break; }
+                gcur = it.g;
+                set_divisor(gcur);
+                queries(gcur, false);
             }
             if (C::ALT && (e & 1) != group) continue;
             const int st = e % NSK, j0 = it.tile * KT;
             unsigned char* kt = smem + C::K0 + st * C::TILE;
             const bool drafted = j0 + KT > L;
-            // turned position of a row: its place, or a drafted row's depth, over the
-            // group size (rows past the end: 0, they are masked)
-            auto turned = [&](int r) {
-                const int j = j0 + r;
-                uint32_t pos = (uint32_t)j;
-                if (drafted && j >= L) pos = j < n ? (uint32_t)(L + depth[j - L]) : 0u;
+            auto over_g = [&](uint32_t pos) {
                 const uint32_t t1 = __umulhi(dm, pos);
                 return (t1 + ((pos - t1) >> ds1)) >> ds2;
             };
-            uint32_t f = turned(row0);
-            float2 cs[4], sn[4];
-            angles(f, cs, sn);
+            // Keys are rounded to fp16 as they are, unless one of the warp's is too large
+            // for it (0x4700: 2^15), or the query makes small ones count: then every row is
+            // first scaled by its own power of two.  `top` covers the rows at hand.
             unsigned scaled = 0;
-            if (!ro.wait(&bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
-            // from row to row the turned position stays or steps by one (drafted
-            // rows may jump): the angles follow by the angle addition
-            auto advance = [&](int r) {
-                const uint32_t fn = turned(r);
-                if (fn == f + 1) {
+            auto too_large = [&](uint32_t top) { return __any_sync(0xffffffffu, always || mag16(top) >= 0x4700u); };
+            auto scale_row = [&](uint4& lo, uint4& hi) {
+                uint32_t m = mag16(absmax8(lo, hi));
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float2 ns = make_float2(-sn[u].x, -sn[u].y);
-                        const float2 nc = fma2(ns, sts[u], mul2(cs[u], stc[u]));
-                        sn[u] = fma2(cs[u], sts[u], mul2(sn[u], stc[u]));
-                        cs[u] = nc;
-                    }
-                } else if (fn != f) {
-                    angles(fn, cs, sn);
-                }
-                f = fn;
+                for (int o = 1; o < CH; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const int ex = tc::range_exp(m);
+                scale8(lo, tc::pow2i(ex));
+                scale8(hi, tc::pow2i(ex));
+                scaled = 1;
+                return tc::pow2i(-ex);
             };
-#pragma unroll 1
-            for (int x = 0; x < RPT; x += 2) {
-                const int r = row0 + x;
-                uint4* pa = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c));
-                uint4* pb = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c + CH));
-                uint4* pc = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r + 1, c));
-                uint4* pd = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r + 1, c + CH));
-                uint4 a0 = *pa, b0 = *pb, a1 = *pc, b1 = *pd;
-                // Keys are rounded to fp16 as they are, unless one of the warp's is too
-                // large for it (0x4700: 2^15), or the query makes small ones count: then
-                // every row is first scaled by its own power of two.
-                uint32_t m0 = absmax8(a0, b0), m1 = absmax8(a1, b1);
-                float k0 = 1.f, k1 = 1.f;
-                if (__any_sync(0xffffffffu, always || mag16(absmax2(m0, m1)) >= 0x4700u)) {
-                    scaled = 1;
-                    m0 = mag16(m0);
-                    m1 = mag16(m1);
+            float* kscale = ksc + (e % INFO) * KT;
+            Angles by;
+            if (!drafted) {
+                // committed rows: the turned position of row j is floor(j / g); from row to
+                // row it stays or steps by one, and the angles follow by angle addition.
+                // (The loop body is kept small: five roles share the instruction cache, and
+                // with four rows per turn the 128K batch took 1130 us instead of 810.)
+                uint32_t f = over_g((uint32_t)(j0 + row0));
+                angles(f, by);
+                if (!ro.wait(&bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
+                auto advance = [&](int r) {
+                    const uint32_t fn = over_g((uint32_t)(j0 + r));
+                    if (fn != f) {
 #pragma unroll
-                    for (int o = 1; o < CH; o <<= 1) {
-                        m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                        m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                        for (int u = 0; u < 4; ++u) {
+                            const float2 nc = fma2(make_float2(-by.sn[u].x, -by.sn[u].y), sts[u], mul2(by.cs[u], stc[u]));
+                            by.sn[u] = fma2(by.cs[u], sts[u], mul2(by.sn[u], stc[u]));
+                            by.cs[u] = nc;
+                        }
                     }
-                    const int e0 = tc::range_exp(m0), e1 = tc::range_exp(m1);
-                    scale8(a0, tc::pow2i(e0));
-                    scale8(b0, tc::pow2i(e0));
-                    scale8(a1, tc::pow2i(e1));
-                    scale8(b1, tc::pow2i(e1));
-                    k0 = tc::pow2i(-e0);
-                    k1 = tc::pow2i(-e1);
+                    f = fn;
+                };
+#pragma unroll 1
+                for (int x = 0; x < RPT; x += 2) {
+                    const int r = row0 + x;
+                    uint4* pa = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c));
+                    uint4* pb = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c + CH));
+                    uint4* pc = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r + 1, c));
+                    uint4* pd = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r + 1, c + CH));
+                    uint4 a0 = *pa, b0 = *pb, a1 = *pc, b1 = *pd;
+                    float2 ks = make_float2(1.f, 1.f);
+                    if (too_large(absmax2(absmax8(a0, b0), absmax8(a1, b1)))) {
+                        ks.x = scale_row(a0, b0);
+                        ks.y = scale_row(a1, b1);
+                    }
+                    if (c == 0) *reinterpret_cast<float2*>(kscale + r) = ks;
+                    if (x > 0) advance(r);
+                    turn(a0, b0, by);
+                    *pa = a0;
+                    *pb = b0;
+                    advance(r + 1);
+                    turn(a1, b1, by);
+                    *pc = a1;
+                    *pd = b1;
                 }
-                if (c == 0) *reinterpret_cast<float2*>(ksc + (e % INFO) * KT + r) = make_float2(k0, k1);
-                if (x > 0) advance(r);
-                turn(a0, b0, cs, sn);
-                *pa = a0;
-                *pb = b0;
-                advance(r + 1);
-                turn(a1, b1, cs, sn);
-                *pc = a1;
-                *pd = b1;
+            } else {
+                // a request's last tiles: drafted rows sit at their depths (rows past the
+                // end: 0, they are masked)
+                if (!ro.wait(&bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
+#pragma unroll 1
+                for (int x = 0; x < RPT; ++x) {
+                    const int r = row0 + x, j = j0 + r;
+                    angles(over_g(j < L ? (uint32_t)j : j < n ? (uint32_t)(L + depth[j - L]) : 0u), by);
+                    uint4* pa = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c));
+                    uint4* pb = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c + CH));
+                    uint4 a = *pa, b = *pb;
+                    float ks = 1.f;
+                    if (too_large(absmax8(a, b))) ks = scale_row(a, b);
+                    if (c == 0) kscale[r] = ks;
+                    turn(a, b, by);
+                    *pa = a;
+                    *pb = b;
+                }
             }
             if (lane == 0) reinterpret_cast<volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 4 + (rt >> 5)] = scaled;
             fence_proxy_async_smem();
