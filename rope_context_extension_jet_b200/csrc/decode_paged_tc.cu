@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
         constexpr uint32_t IQK = idesc_f16(KT, NCOL, 0);
         constexpr uint32_t IPV = idesc_bf16(128, C::NPV, 1) | (1u << 15);  // A (V^T) and B (P^T) both MN-major
         const uint32_t sb = smem_u32(smem);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         int e = 0;
         unsigned nfix = 0;  // per stage: parity of the repaired value tiles so far
         bool ok = true;
@@ -124,18 +125,12 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 nfix ^= 1u << st;
             }
             tc_fence_after();
-            if (lane == 0) {
-                // d = 64: the second 64-column atom of V^T is whatever follows the
-                // tile; it fills lanes 64..127 of O^T, which nothing reads
-                const uint64_t a = sdesc_sw128(sb + C::V0 + st * C::TILE, C::ATOM_K, 1024);
-                const uint64_t bd = sdesc_sw128(sb + C::P0 + (x % C::NP) * C::PBYTES, C::ATOM_K, 1024);
-#pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    umma_ss(tmem + 2 * TS, a + 128 * k, bd + 128 * k, IPV, !(first && k == 0));
-                umma_commit(&bars.vempty[st]);
-                umma_commit(&pvdone[x & 1]);
-            }
-            __syncwarp();
+            // d = 64: the second 64-column atom of V^T is whatever follows the tile; it
+            // fills lanes 64..127 of O^T, which nothing reads
+            umma_ss_mn128(tm + 2 * TS, sdesc_sw128(sb + C::V0 + st * C::TILE, C::ATOM_K, 1024),
+                          sdesc_sw128(sb + C::P0 + (x % C::NP) * C::PBYTES, C::ATOM_K, 1024), IPV, first ? 0u : 1u);
+            umma_commit_elect(&bars.vempty[st]);
+            umma_commit_elect(&pvdone[x & 1]);
             return true;
         };
         bool pend = false, pfirst = false, pfix = false;
@@ -158,17 +153,12 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 if (!ro.wait(&bars.kready[st], (e / NSK) & 1, 0x414)) { ok = false; break; }
                 const bool fix = (it.tile + 1) * KT > L || ro.note()[e % INFO] != all_pages;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t a = sdesc_sw128(sb + C::K0 + st * C::TILE, 16, 1024);
-                    const uint64_t bq = sdesc_sw128(sb + C::Q0, 16, 1024);
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x)
-                        umma_ss(tmem + (e & 1) * TS, a + (x >> 2) * (C::ATOM_K / 16) + (x & 3) * 2,
-                                bq + (x >> 2) * (C::ATOM_Q / 16) + (x & 3) * 2, IQK, x != 0);
-                    umma_commit(&bars.kempty[st]);
-                    umma_commit(&sfull[e & 1]);
-                }
-                __syncwarp();
+                const uint64_t a = sdesc_sw128(sb + C::K0 + st * C::TILE, 16, 1024);
+                const uint64_t bq = sdesc_sw128(sb + C::Q0, 16, 1024);
+                umma_ss_k64(tm + (e & 1) * TS, a, bq, IQK, 0u);
+                if (D == 128) umma_ss_k64(tm + (e & 1) * TS, a + C::ATOM_K / 16, bq + C::ATOM_Q / 16, IQK, 1u);
+                umma_commit_elect(&bars.kempty[st]);
+                umma_commit_elect(&sfull[e & 1]);
                 if (pend && !pv(e - 1, pfirst, pfix)) { ok = false; break; }
                 pend = true;
                 pfirst = first;
@@ -178,8 +168,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             ro.unit_done(k);
         }
         if (ok && pend) pv(e - 1, pfirst, pfix);
-        if (lane == 0) umma_commit(bars.drain);
-        __syncwarp();
+        umma_commit_elect(bars.drain);
         mbar_wait(bars.drain, 0);
     } else if (warp < 12) {
         rotate_keys<C>(ro);

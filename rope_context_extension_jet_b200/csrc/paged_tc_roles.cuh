@@ -186,17 +186,33 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
           "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 
-// One MMA (one thread issues): D[tmem] (+)= A B, operands in shared memory.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// Groups of MMAs from one elected lane of a converged warp, D[tmem] (+)= A B with both
+// operands in shared memory; the descriptors of later steps are the first one's plus
+// immediates (16-byte units; no carry out of the address field).  Issued one by one
+// from a single thread, the 16 MMAs of a tile took 2500 cycles, most of a tile's time.
+#define JL_SS(AO, BO, ACC)                                                                                          \
+    "add.u32 al, %1, " AO ";\n\tadd.u32 bl, %3, " BO ";\n\tmov.b64 da, {al, %2};\n\tmov.b64 db, {bl, %4};\n\t"       \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, " ACC ";\n\t"
+#define JL_SS_HEAD                                                                                                   \
+    "{\n\t.reg .pred p, t, e;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\telect.sync _|e, 0xffffffff;\n\t"          \
+    "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+#define JL_SS_ARGS                                                                                                   \
+    "}" ::"r"(d), "r"((uint32_t)a), "r"((uint32_t)(a >> 32)), "r"((uint32_t)b), "r"((uint32_t)(b >> 32)), "r"(idesc), "r"(acc)
+// K-major operands over 64 of the head dimensions (four steps inside one swizzle atom)
+__device__ __forceinline__ void umma_ss_k64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile(JL_SS_HEAD JL_SS("0", "0", "p") JL_SS("2", "2", "t") JL_SS("4", "4", "t") JL_SS("6", "6", "t") JL_SS_ARGS : "memory");
 }
-__device__ __forceinline__ void umma_commit(uint64_t* bar)
+// MN-major operands over 128 keys (eight steps of 16 rows of 128 bytes)
+__device__ __forceinline__ void umma_ss_mn128(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile(JL_SS_HEAD JL_SS("0", "0", "p") JL_SS("128", "128", "t") JL_SS("256", "256", "t") JL_SS("384", "384", "t")
+                     JL_SS("512", "512", "t") JL_SS("640", "640", "t") JL_SS("768", "768", "t") JL_SS("896", "896", "t")
+                         JL_SS_ARGS : "memory");
 }
+#undef JL_SS
+#undef JL_SS_HEAD
+#undef JL_SS_ARGS
 
 __device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b)
 {
