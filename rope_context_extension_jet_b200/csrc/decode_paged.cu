@@ -77,7 +77,6 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
 
     piece_plan<PS_KT, RT, PS_NT>(p, 2, plan, reinterpret_cast<long long*>(plan + 1));
     if (tid == 0) clear_cut(p);
-    let_merge_start();
     long long cur = plan->start, base = plan->base;
     const long long end = plan->end;
     int b = plan->b;
@@ -387,7 +386,8 @@ __global__ void __launch_bounds__(MG_NT) decode_paged_merge_kernel(PagedProblem 
 
 int merge_rows(const PagedProblem& p, int rt) { return (std::min(rt, p.max_nodes * p.group) + MG_ROWS - 1) / MG_ROWS; }
 
-// Starts while the attention kernel runs and waits for its end on the device.
+// Programmatic launch: the merge is set up while the attention kernel ends (an early
+// trigger in that kernel gained 0.2 us of 18 on the smallest call and is left out).
 template <class Kern>
 cudaError_t launch_after(Kern kern, dim3 grid, int nthr, cudaStream_t st, const PagedProblem& p)
 {

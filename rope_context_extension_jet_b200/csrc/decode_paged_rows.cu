@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (un->rows == 0) break;
                 const int L = un->L;
                 int gcur = -1, li = 0;
-                for (UnitItems it(un); ok && it.left > 0; it.next(un), ++e, ++li) {
+                for (UnitItems it(un); ok && it.left > 0; it.next(), ++e, ++li) {
                     const int st = e % NSK;
                     bool fix = false;
                     for (int s = PAIR ? 0 : li & 1, s1 = PAIR ? 1 : s; s <= s1; ++s) {
@@ -190,10 +190,12 @@ __global__ void __launch_bounds__(512, 1)
             float ref = kNoRef, l = 0.f;
             unsigned long long nodes = 0;  // drafted nodes this row attends in the current phase
             int gcur = -1, li = 0, mine = 0;
+            const int L = ud->L, T = ud->T, near = L + T - 1 - ud->w0;
+            const int far = ud->ng > 1 ? -1 : (int)max(-1ll, (long long)L - ud->w0 - (KT - 1));
             if (ok) {
-                for (UnitItems it(ud); it.left > 0; it.next(ud), ++e, ++li) {
+                for (UnitItems it(ud); it.left > 0; it.next(), ++e, ++li) {
                     if (!PAIR && (li & 1) != s) continue;
-                    const int g = it.g, j0 = it.tile * KT, L = ud->L, T = ud->T;
+                    const int g = it.g, j0 = it.tile * KT;
                     if (!ro.wait(&sfull[s], done & 1, 0x532)) { ok = false; break; }
                     tc_fence_after();
                     float x[KT];
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(512, 1)
                         }
                     }
                     const bool drafted = j0 + KT > L || have != all_pages;
-                    if (drafted || (g == 0 ? L + T - 1 - j0 >= ud->w0 : (ud->ng > 1 || L - (j0 + KT - 1) < ud->w0))) {
+                    if (drafted || (g == 0 ? j0 <= near : j0 > far)) {
                         asm volatile("" ::: "memory");  // a branch, not predication: most tiles skip this
                         if (g != gcur) {
                             gcur = g;

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             const int L = un->L;
             int gcur = -1;
             bool first = true;
-            for (UnitItems it(un); it.left > 0; it.next(un), ++e) {
+            for (UnitItems it(un); it.left > 0; it.next(), ++e) {
                 const int st = e % NSK;
                 if (it.g != gcur) {
                     gcur = it.g;
@@ -210,11 +210,14 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 zero[key] = 0.f;
             }
             if (named_or(bid, 128, !ok)) break;
-            const int cols = ud->rows;
-            const int L = ud->L;
+            const int cols = ud->rows, L = ud->L, n = L + ud->T;
+            // an exact item has pairs of the other branch up to tile edge `near`, a remote
+            // one past `far` (always, where group sizes differ)
+            const int near = n - 1 - ud->w0;
+            const int far = ud->ng > 1 ? -1 : (int)max(-1ll, (long long)L - ud->w0 - (KT - 1));
             bool first = true;
-            for (UnitItems it(ud); it.left > 0; it.next(ud), ++e) {
-                const int g = it.g, j0 = it.tile * KT, n = L + ud->T;
+            for (UnitItems it(ud); it.left > 0; it.next(), ++e) {
+                const int g = it.g, j0 = it.tile * KT;
                 ok = ok && ro.wait(&sfull[e & 1], (e >> 1) & 1, 0x432);
                 tc_fence_after();
                 const unsigned have = ro.note()[e % INFO];
@@ -222,9 +225,11 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 // incomplete tile's; the other branch's on the border of the window
                 // (or of columns with another group size)
                 const bool drafted = j0 + KT > L || have != all_pages;
-                const bool masked = drafted || (g == 0 ? n - 1 - j0 >= ud->w0 : (ud->ng > 1 || L - (j0 + KT - 1) < ud->w0));
-                const float ks = *reinterpret_cast<const volatile float*>(ksc + (e % INFO) * KT + key);
-                const bool any_scaled = __any_sync(0xffffffffu, ks != 1.f);
+                const bool masked = drafted || (g == 0 ? j0 <= near : j0 > far);
+                // rotation warp wl scaled some of this warp's key rows
+                const bool any_scaled = reinterpret_cast<const volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 4 + wl] != 0;
+                float ks = 1.f;
+                if (any_scaled) ks = *reinterpret_cast<const volatile float*>(ksc + (e % INFO) * KT + key);
                 const int j = j0 + key, u = j - L;
                 const bool there = j < n && ((have >> (key >> gshift)) & 1);
                 uint32_t keep = 0;  // masked tiles: one bit per column
@@ -348,11 +353,9 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 }
                 if (stop) break;
                 first = false;
-                // weights to the P buffer, free once P V of item e - NP is done
-                if (e >= C::NP) {
-                    const int x = e - C::NP;
-                    ok = ro.wait(&pvdone[x & 1], (x >> 1) & 1, 0x434);
-                }
+                // weights to the P buffer e % 2: P V of item e - 2, its last reader, was issued
+                // before Q K^T of this item, whose commit (sfull) covers every earlier MMA
+                static_assert(C::NP == 2, "P buffers");
                 unsigned char* pb = smem + C::P0 + (e % C::NP) * C::PBYTES + key * 128;
                 {
 #pragma unroll

@@ -102,10 +102,6 @@ size_t paged_tc_workspace(int rows, int d);
 cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s, int* grid);
 cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch);
 
-// Lets the merge kernel's CTAs start where there is room; they wait on the device
-// for the end of this grid.
-__device__ __forceinline__ void let_merge_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 __device__ __forceinline__ void record_input(int* word, int code)
 {
     if (word) atomicCAS(word, 0, code);

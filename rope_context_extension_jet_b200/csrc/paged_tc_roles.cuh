@@ -136,26 +136,32 @@ struct Bars {
 // The items of a unit in order: the group size its keys are aliased by (0: exact
 // positions) and the key tile.
 struct UnitItems {
-    int g, tile, left;
+    int g, tile, left, nR, kE0, gend;
     __device__ __forceinline__ explicit UnitItems(UnitPtr u)
     {
-        const int i = u->i0, nR = u->nR, rem = u->ng * nR;
+        const int i = u->i0, rem = u->ng * u->nR;
+        nR = u->nR;
+        kE0 = u->kE0;
+        gend = u->gmin + u->ng;
         left = u->i1 - i;
         g = 0;
-        tile = u->kE0 + (i - rem);
+        tile = kE0 + (i - rem);
         if (i < rem) {
             g = u->gmin + i / nR;
             tile = i % nR;
         }
     }
-    __device__ __forceinline__ void next(UnitPtr u)
+    __device__ __forceinline__ void next()
     {
         --left;
         ++tile;
-        if (g != 0 && tile == u->nR) {
-            const bool more = g + 1 < u->gmin + u->ng;
-            tile = more ? 0 : u->kE0;
-            g = more ? g + 1 : 0;
+        if (g != 0 && tile == nR) {
+            ++g;
+            tile = 0;
+            if (g == gend) {
+                g = 0;
+                tile = kE0;
+            }
         }
     }
 };
@@ -236,6 +242,8 @@ struct Role {
     __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(smem_base() + C::SLOT + 4); }
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int code) const
     {
+        // (the whole warp polls: one lane polling for the others took 10-40% longer, and
+        // letting the hardware park the warp 10%)
         return tc::warp_wait(bar, parity, abort_flag(), ln.dev_error, ln.wait_cycles, code);
     }
     // unit k of the piece: wait until it is planned; afterwards each warp hands it back
@@ -275,7 +283,6 @@ __device__ __forceinline__ uint32_t start_cta(const Role<C>& ro, InitExtra init_
     piece_plan<KT, C::ROWS, C::THREADS>(ro.p, ro.ln.min_items, reinterpret_cast<PiecePlan*>(smem_base() + C::PLAN),
                                         reinterpret_cast<long long*>(smem_base() + C::SCAN));
     tc_fence_after();
-    let_merge_start();
     return *slot;
 }
 
@@ -303,7 +310,7 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
         if (un->rows == 0) break;
         const int* table = p.table + (size_t)un->b * p.max_pages;
         const int n = un->L + un->T, kvh = un->kvh;
-        for (UnitItems it(un); it.left > 0; it.next(un), ++e) {
+        for (UnitItems it(un); it.left > 0; it.next(), ++e) {
             // lane x looks after rows [x box, (x + 1) box) of the tile
             const int row = it.tile * KT + lane * box;
             const bool want = lane * box < KT && row < n;
@@ -591,7 +598,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             ds2 = lg > 1 ? lg - 1 : 0;
         };
         set_divisor(gcur);
-        for (; it.left > 0; it.next(ud), ++e) {
+        for (; it.left > 0; it.next(), ++e) {
             if (it.g != gcur) {
                 // the next phase; the tensor cores are done with the queries of the last
                 if (!ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423)) { ok = false; break; }
