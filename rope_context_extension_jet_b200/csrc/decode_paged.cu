@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
         const bool whole = i0 == 0 && i1 == s.items;
         if (tid == 0 && i0 == 0 && !whole) note_cut(p, s, plan->per, cur, kvh, r0, nrows);
         float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
-                      ((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * RT * (D + 2);
+                      ((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * RT * (D + 4);
         float* red = kr;  // [KS][8][D] = PS_NT * 32 floats: fits kr and vs together
 #pragma unroll
         for (int rg = 0; rg < RT; rg += 8) {
@@ -288,8 +288,8 @@ __global__ void __launch_bounds__(PS_NT, RT <= 8 ? 2 : 1) decode_paged_simt_kern
                     const int node = (r0 + r) / p.group, hd = kvh * p.group + (r0 + r) % p.group;
                     store_elem(static_cast<T*>(p.out) + ((size_t)(s.n0 + node) * p.Hq + hd) * D + c, acc / sl[r]);
                 } else {
-                    part[(size_t)r * (D + 2) + c] = acc;
-                    if (c < 2) part[(size_t)r * (D + 2) + D + c] = c == 0 ? sm[r] : sl[r];
+                    part[(size_t)r * (D + 4) + c] = acc;
+                    if (c < 2) part[(size_t)r * (D + 4) + D + c] = c == 0 ? sm[r] : sl[r];
                 }
             }
         }
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(MG_NT) decode_paged_merge_kernel(PagedProblem 
 #pragma unroll
     for (int u = 0; u < V; ++u) o[u] = 0.f;
     // piece x: slot 2 c + 1 of the CTA that begins the unit, slot 2 (c + x) of the others
-    auto piece = [&](int x) { return parts + ((size_t)(2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)) * RT + r) * (D + 2); };
+    auto piece = [&](int x) { return parts + ((size_t)(2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)) * RT + r) * (D + 4); };
     if (r < rows) {
         const int each = (pieces + MG_SPLIT - 1) / MG_SPLIT, x1 = min(pieces, (sub + 1) * each);
         for (int x0 = sub * each; x0 < x1; x0 += 32) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(MG_NT) decode_paged_merge_kernel(PagedProblem 
                 const float* row = piece(x0 + x) + lane * V;
                 if (wx != 0.f) {  // a piece without a key of this row holds no values
 #pragma unroll
-                    for (int u = 0; u < V; u += 2) {
+                    for (int u = 0; u < V; u += 2) {  // (lane * V: 8-byte aligned for d = 64)
                         const float2 v = __ldcg(reinterpret_cast<const float2*>(row + u));
                         o[u] = fmaf(wx, v.x, o[u]);
                         o[u + 1] = fmaf(wx, v.y, o[u + 1]);
@@ -463,7 +463,7 @@ cudaError_t run_bf16(const PagedProblem& p, cudaStream_t st, int* nlaunch)
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_nodes)
 {
     const int rows = max_nodes * (Hq / Hkv);
-    const size_t simt = (size_t)kSimtCtas * 2 * (rows <= 8 ? 8 : 16) * (d + 2) * sizeof(float);
+    const size_t simt = (size_t)kSimtCtas * 2 * (rows <= 8 ? 8 : 16) * (d + 4) * sizeof(float);
     return kPagedHeader + std::max(simt, paged_tc_workspace(rows, d));
 }
 

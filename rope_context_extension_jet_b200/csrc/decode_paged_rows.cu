@@ -15,9 +15,10 @@
 //   ROWS = 128: both hold the same rows and take the tiles in turn; each keeps its
 //     own reference, sum and O, joined where the unit ends.
 //
-// Warp roles: 0 / 3 producers, 1 MMA issuer, 2 tensor memory and planner, 4-7
-// rotation, 8-11 / 12-15 softmax of stream 0 / 1.
-// TMEM (512 columns): S_0, S_1 (128 each; P_s over the first 64 of S_s), O_0, O_1.
+// Warp roles: 0 / 3 producers, 1 MMA issuer, 2 tensor memory and planner, 4-11
+// rotation, 12-15 / 16-19 softmax of stream 0 / 1.
+// TMEM (512 columns): S_0, S_1 (128 each; the halves of P_s over columns 0-31 and
+// 64-95 of S_s, each over the half of S_s it was made from), O_0, O_1.
 #include <algorithm>
 
 #include "paged_tc_roles.cuh"
@@ -30,9 +31,11 @@ template <int D, int NROWS>
 struct RowTiles {
     static constexpr int DIM = D, ROWS = NROWS;
     static constexpr int NSK = D == 64 ? 4 : NROWS == 128 ? 3 : 2, NSV = D == 64 ? 4 : 2;
-    static constexpr int THREADS = 512;
-    static constexpr bool ALT = false;
-    static constexpr int ROT = 128, ROTALL = 128, SOFT = 8;
+    static constexpr int THREADS = 640;
+    // two rotation warpgroups: in turn where the ring has three key stages, else
+    // sharing each tile.  (One alone took 4200 cycles a tile and bounded the kernel.)
+    static constexpr bool ALT = NSK >= 3;
+    static constexpr int ROT = ALT ? 128 : 256, ROTALL = 256, SOFT = 8;
     static constexpr int ATOMS = D / 64;
     static constexpr int TILE = KT * D * 2, ATOM_K = KT * 128;
     static constexpr int K0 = 0, V0 = K0 + NSK * TILE, Q0 = V0 + NSV * TILE, BASE = Q0 + NROWS * D * 2;
@@ -40,19 +43,19 @@ struct RowTiles {
 };
 template <int D, int NROWS>
 struct RowCfg : RowTiles<D, NROWS>,
-                Notes<D, NROWS, RowTiles<D, NROWS>::NSK, RowTiles<D, NROWS>::NSV, RowTiles<D, NROWS>::BASE, 8, 16> {
+                Notes<D, NROWS, RowTiles<D, NROWS>::NSK, RowTiles<D, NROWS>::NSV, RowTiles<D, NROWS>::BASE, 8, 20> {
     static constexpr int XCH = RowCfg::NOTES_END;  // [2][128] (reference, sum) of the streams
     static constexpr int TOTAL = XCH + 2 * 128 * 8 + 1024;
     static_assert(TOTAL <= 232448, "shared memory");
-    // Registers per thread after setmaxnreg: producers / issuer / planner, rotation,
-    // each softmax warpgroup.  An increase draws on what the block was launched with
-    // (512 x 128).
-    static constexpr int R_PROD = 56, R_ROT = 104, R_SOFT = 176;
-    static_assert((R_PROD + R_ROT + 2 * R_SOFT) * 128 <= 512 * 128, "register split");
+    // Registers per thread after setmaxnreg: producers / issuer / planner, the two
+    // rotation and the two softmax warpgroups.  640 threads launch with 96 each, and an
+    // increase draws on that.
+    static constexpr int R_PROD = 40, R_ROT = 88, R_SOFT = 128;
+    static_assert((R_PROD + 2 * R_ROT + 2 * R_SOFT) * 128 <= 640 * 96, "register split");
 };
 
 template <int D, int NROWS>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(640, 1)
     decode_paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                              const __grid_constant__ PagedProblem p, const Launch ln)
 {
@@ -104,10 +107,10 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 const uint64_t vd = sdesc_sw128(sb + C::V0 + st * C::TILE, C::ATOM_K, 1024);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int half = 1; half >= 0; --half) {  // in the order the softmax publishes them
                     if (!ro.wait(&pfull[2 * s + half], done[s] & 1, 0x511)) return false;
                     tc_fence_after();
-                    umma_pv_k64(tm + 256 + s * 128, tm + s * 128 + 32 * half, vd + 512 * half, IPV, pfirst[s] && half == 0 ? 0u : 1u);
+                    umma_pv_k64(tm + 256 + s * 128, tm + s * 128 + 64 * half, vd + 512 * half, IPV, pfirst[s] && half == 1 ? 0u : 1u);
                 }
                 umma_commit_elect(&pvdone[s]);
                 if (!PAIR || s == 1) umma_commit_elect(&bars.vempty[st]);
@@ -156,14 +159,14 @@ __global__ void __launch_bounds__(512, 1)
             umma_commit_elect(bars.drain);
             mbar_wait(bars.drain, 0);
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         regs_dec<C::R_ROT>();
         rotate_keys<C>(ro);
     } else {
         regs_inc<C::R_SOFT>();
         // ------------------------------------------------------ softmax
         constexpr int bid = 2;  // named barrier of both warpgroups
-        const int s = (warp - 8) >> 2, lrow = (warp & 3) * 32 + lane, row = (PAIR ? s * 128 : 0) + lrow;
+        const int s = (warp - 12) >> 2, lrow = (warp & 3) * 32 + lane, row = (PAIR ? s * 128 : 0) + lrow;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t s_col = lanes + s * 128, o_col = lanes + 256 + s * 128;
         const float* ksc = reinterpret_cast<const float*>(smem + C::KSC);
@@ -198,39 +201,15 @@ __global__ void __launch_bounds__(512, 1)
                     const int g = it.g, j0 = it.tile * KT;
                     if (!ro.wait(&sfull[s], done & 1, 0x532)) { ok = false; break; }
                     tc_fence_after();
-                    float x[KT];
-                    {
-                        uint32_t t0[32], t1[32], t2[32], t3[32];  // four loads in flight, one wait
-                        tmem_ld32(s_col, t0);
-                        tmem_ld32(s_col + 32, t1);
-                        tmem_ld32(s_col + 64, t2);
-                        tmem_ld32(s_col + 96, t3);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) {
-                            x[u] = __uint_as_float(t0[u]);
-                            x[32 + u] = __uint_as_float(t1[u]);
-                            x[64 + u] = __uint_as_float(t2[u]);
-                            x[96 + u] = __uint_as_float(t3[u]);
-                        }
-                    }
                     const unsigned have = ro.note()[e % INFO];
-                    const volatile unsigned* sc4 = reinterpret_cast<const volatile unsigned*>(smem + C::SCALED) + (e % INFO) * 4;
-                    if ((sc4[0] | sc4[1]) | (sc4[2] | sc4[3])) {
-                        // some key rows were scaled by a power of two (paged_tc_roles.cuh)
-                        asm volatile("" ::: "memory");
-                        const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT);
+                    const volatile unsigned* flags = reinterpret_cast<const volatile unsigned*>(smem + C::SCALED) + (e % INFO) * 8;
+                    unsigned any_scaled = 0;  // one flag per rotation warp of the tile
 #pragma unroll
-                        for (int u = 0; u < KT; u += 4) {
-                            const float4 f = k4[u / 4];
-                            x[u] *= f.x;
-                            x[u + 1] *= f.y;
-                            x[u + 2] *= f.z;
-                            x[u + 3] *= f.w;
-                        }
-                    }
+                    for (int w = 0; w < C::ROT / 32; ++w) any_scaled |= flags[w];
                     const bool drafted = j0 + KT > L || have != all_pages;
-                    if (drafted || (g == 0 ? j0 <= near : j0 > far)) {
+                    const bool masked = drafted || (g == 0 ? j0 <= near : j0 > far);
+                    uint32_t bits[4];  // masked tiles: the keys of the tile that belong to this row and item
+                    if (masked) {
                         asm volatile("" ::: "memory");  // a branch, not predication: most tiles skip this
                         if (g != gcur) {
                             gcur = g;
@@ -245,44 +224,90 @@ __global__ void __launch_bounds__(512, 1)
                         // committed keys: those past the border (exact phase) or up to it
                         // (remote phase of this row's group size), before row L
                         const int cut = lim < j0 ? 0 : lim - j0 + 1;  // keys [0, cut) of the tile are remote
-                        const int c0 = L - j0;         // keys [0, c0) are committed
+                        const int c0 = L - j0;                        // keys [0, c0) are committed
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             auto below = [&](int n) {  // bits of this word's keys that lie in [0, n) of the tile
                                 const int m = n - 32 * w;
                                 return m <= 0 ? 0u : m >= 32 ? 0xffffffffu : (1u << m) - 1;
                             };
-                            uint32_t bits = below(cut);
-                            bits = g == 0 ? ~bits : (G == g ? bits : 0u);
-                            bits &= below(c0);
+                            uint32_t o = below(cut);
+                            o = g == 0 ? ~o : (G == g ? o : 0u);
+                            o &= below(c0);
                             // node v is key c0 + v
                             const int sh = 32 * w - c0;
                             if (sh >= 0)
-                                bits |= sh < 64 ? (uint32_t)(nodes >> sh) : 0u;
+                                o |= sh < 64 ? (uint32_t)(nodes >> sh) : 0u;
                             else if (sh > -32)
-                                bits |= (uint32_t)nodes << -sh;
+                                o |= (uint32_t)nodes << -sh;
                             if (have != all_pages) {
                                 uint32_t there = 0;
 #pragma unroll 1
                                 for (int u = 0; u < 32; ++u) there |= ((have >> ((32 * w + u) >> gshift)) & 1u) << u;
-                                bits &= there;
+                                o &= there;
                             }
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) x[32 * w + u] = (bits >> u) & 1 ? x[32 * w + u] : -INFINITY;
+                            bits[w] = o;
                         }
+                        __syncwarp();
                     }
-                    float m4[4] = {x[0], x[1], x[2], x[3]};
+                    // 64 keys of the row; key rows that were scaled by a power of two
+                    // (paged_tc_roles.cuh) scaled back, what does not belong at -inf
+                    float x[KT / 2];
+                    auto load = [&](int half) {
+                        {
+                            uint32_t t0[32], t1[32];
+                            tmem_ld32(s_col + half * 64, t0);
+                            tmem_ld32(s_col + half * 64 + 32, t1);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int u = 4; u < KT; u += 8) {
-                        m4[0] = fmax3(m4[0], x[u], x[u + 1]);
-                        m4[1] = fmax3(m4[1], x[u + 2], x[u + 3]);
-                        if (u + 4 < KT) {
-                            m4[2] = fmax3(m4[2], x[u + 4], x[u + 5]);
-                            m4[3] = fmax3(m4[3], x[u + 6], x[u + 7]);
+                            for (int u = 0; u < 32; ++u) {
+                                x[u] = __uint_as_float(t0[u]);
+                                x[32 + u] = __uint_as_float(t1[u]);
+                            }
                         }
+                        if (any_scaled) {
+                            asm volatile("" ::: "memory");
+                            const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT + half * 64);
+#pragma unroll
+                            for (int u = 0; u < KT / 2; u += 4) {
+                                const float4 f = k4[u / 4];
+                                x[u] *= f.x;
+                                x[u + 1] *= f.y;
+                                x[u + 2] *= f.z;
+                                x[u + 3] *= f.w;
+                            }
+                        }
+                        if (masked) {
+                            asm volatile("" ::: "memory");
+                            const uint32_t b0 = half ? bits[2] : bits[0], b1 = half ? bits[3] : bits[1];
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) {
+                                x[u] = (b0 >> u) & 1 ? x[u] : -INFINITY;
+                                x[32 + u] = (b1 >> u) & 1 ? x[32 + u] : -INFINITY;
+                            }
+                        }
+                    };
+                    // the row's largest logit over both halves; the second stays in registers
+                    // (half the tile at a time keeps the softmax at 128 registers, which is
+                    // what makes room for two rotation warpgroups)
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        load(half);
+                        float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                        for (int u = 4; u < KT / 2; u += 8) {
+                            m4[0] = fmax3(m4[0], x[u], x[u + 1]);
+                            m4[1] = fmax3(m4[1], x[u + 2], x[u + 3]);
+                            if (u + 4 < KT / 2) {
+                                m4[2] = fmax3(m4[2], x[u + 4], x[u + 5]);
+                                m4[3] = fmax3(m4[3], x[u + 6], x[u + 7]);
+                            }
+                        }
+                        top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                     }
                     // logits in log2 units: x cq, cq > 0 a power of two times the scale
-                    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cq;
+                    const float mt = top * cq;
                     float alpha = 1.f;
                     const bool resc = mt > ref + kExceed;
                     if (resc) {
@@ -290,40 +315,41 @@ __global__ void __launch_bounds__(512, 1)
                         ref = mt + kAbove;
                         l *= alpha;
                     }
+                    // O is rescaled before any of this tile's P is published
+                    if (mine > 0 && __any_sync(0xffffffffu, resc)) {
+                        if (!ro.wait(&pvdone[s], (done - 1) & 1, 0x533)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int cc = 0; cc < D; cc += 16) {
+                            uint32_t tt[16];
+                            tmem_ld16(o_col + cc, tt);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) tt[u] = __float_as_uint(__uint_as_float(tt[u]) * alpha);
+                            tmem_st16(o_col + cc, tt);
+                        }
+                        tmem_wait_st();
+                    }
                     const float2 sl = make_float2(cq, cq), nm = make_float2(-ref, -ref);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    // the stream's last P V finished before this tile's Q K^T (issued later by
+                    // the same issuer), so each half of P may go over its half of S
+#pragma unroll 1
+                    for (int half = 1; half >= 0; --half) {
+                        if (half == 0) load(0);
                         uint32_t pk[KT / 4];
 #pragma unroll
-                        for (int v = 0; v < KT / 2; v += 4) {
-                            const int u = half * (KT / 2) + v;
+                        for (int u = 0; u < KT / 2; u += 4) {
                             const float2 y0 = fma2(make_float2(x[u], x[u + 1]), sl, nm);
                             const float2 y1 = fma2(make_float2(x[u + 2], x[u + 3]), sl, nm);
                             const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
                             const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
                             acc0 = add2(acc0, p0);
                             acc1 = add2(acc1, p1);
-                            pk[v >> 1] = pack_bf16x2(p0.x, p0.y);
-                            pk[(v >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
+                            pk[u >> 1] = pack_bf16x2(p0.x, p0.y);
+                            pk[(u >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
                         }
-                        // the stream's last P V finished before this tile's Q K^T (issued
-                        // later by the same issuer); O is rescaled before any of this tile's P
-                        // is published
-                        if (half == 0 && mine > 0 && __any_sync(0xffffffffu, resc)) {
-                            if (!ro.wait(&pvdone[s], (done - 1) & 1, 0x533)) { ok = false; break; }
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int cc = 0; cc < D; cc += 16) {
-                                uint32_t tt[16];
-                                tmem_ld16(o_col + cc, tt);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) tt[u] = __float_as_uint(__uint_as_float(tt[u]) * alpha);
-                                tmem_st16(o_col + cc, tt);
-                            }
-                        }
-                        tmem_st32(s_col + half * 32, pk);
+                        tmem_st32(s_col + half * 64, pk);
                         tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
@@ -352,10 +378,10 @@ __global__ void __launch_bounds__(512, 1)
                 l = w0 * l + w1 * o.y;
                 ref = top;
             }
-            const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(un + C::U_BAD) & anc;
+            const unsigned long long bad = ud->bad & anc;
             const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
             float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
-                          (((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NROWS + row) * (D + 2);
+                          (((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NROWS + row) * (D + 4);
             __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + ((size_t)(ud->n0 + node) * p.Hq + hd) * D;
             const float inv = 1.f / l;
             // the streams of one row share its columns
@@ -395,7 +421,8 @@ __global__ void __launch_bounds__(512, 1)
                                        pack_bf16x2(v[8 * q + 4] * inv, v[8 * q + 5] * inv), pack_bf16x2(v[8 * q + 6] * inv, v[8 * q + 7] * inv));
                 } else if (live) {
 #pragma unroll
-                    for (int u = 0; u < 16; u += 2) *reinterpret_cast<float2*>(part + cb + u) = make_float2(v[u], v[u + 1]);
+                    for (int u = 0; u < 16; u += 4)
+                        *reinterpret_cast<float4*>(part + cb + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
                 }
             }
             if (live && !whole && (PAIR || s == 0))
@@ -433,7 +460,7 @@ cudaError_t run_one(const PagedProblem& p, const Launch& ln, cudaStream_t st, in
     });
     if (e != cudaSuccess) return e;
     *grid = std::min(nsm, kTcCtas);
-    kern<<<*grid, 512, smem, st>>>(tk, tv, p, ln);
+    kern<<<*grid, 640, smem, st>>>(tk, tv, p, ln);
     return cudaGetLastError();
 }
 
@@ -453,7 +480,7 @@ int paged_tc_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <=
 
 size_t paged_tc_workspace(int rows, int d)
 {
-    return (size_t)ptc::kTcCtas * 2 * paged_tc_rows(rows) * (d + 2) * sizeof(float);
+    return (size_t)ptc::kTcCtas * 2 * paged_tc_rows(rows) * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s, int* grid)

@@ -9,7 +9,7 @@
 //   O^T [d x RT]        += V^T [d x 128] P^T [128 x RT]       (bf16 operands)
 // both accumulated in fp32 in tensor memory.  A softmax thread owns one key (one
 // TMEM lane) and walks the RT columns, so the weights of a key leave as whole
-// 16-byte chunks; row sums come from a small product of those weights with ones.  The running
+// 16-byte chunks; each thread sums its own key's weights.  The running
 // maximum of a column only has to be near: weights are fp32 / bf16, whose range is
 // far wider than the 2^40 that logits may rise by before it is taken again (kAbove),
 // so each tile costs one vote of the 128 threads, and only a tile that passes the
@@ -22,8 +22,7 @@
 //   warp 2      TMEM allocation; planner: the piece's units, a few ahead, for the others
 //   warps 4-11  per unit: the tree, positions, query scales; per phase: the rotated
 //               queries; per tile: keys rotated in shared memory, in place (angles
-//               advance from row to row); on a request's last tiles, value rows
-//               that do not exist are cleared
+//               advance from row to row)
 //   warps 12-.. softmax, one warpgroup per NCOL columns
 // Every wait on a barrier is bounded as in the prefill kernels.
 #include <algorithm>
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 const bool drafted = j0 + KT > L || have != all_pages;
                 const bool masked = drafted || (g == 0 ? j0 <= near : j0 > far);
                 // rotation warp wl scaled some of this warp's key rows
-                const bool any_scaled = reinterpret_cast<const volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 4 + wl] != 0;
+                const bool any_scaled = reinterpret_cast<const volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 8 + wl] != 0;
                 float ks = 1.f;
                 if (any_scaled) ks = *reinterpret_cast<const volatile float*>(ksc + (e % INFO) * KT + key);
                 const int j = j0 + key, u = j - L;
@@ -394,9 +393,9 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             if (named_or(bid, 128, !ok)) break;
             const int i0 = ud->i0, r0 = ud->r0, kvh = ud->kvh, n0 = ud->n0;
             const bool whole = i0 == 0 && ud->i1 == ud->items;
-            const unsigned long long bad = *reinterpret_cast<const volatile unsigned long long*>(un + C::U_BAD);
+            const unsigned long long bad = ud->bad;
             float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
-                          ((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NCOL * (D + 2);
+                          ((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NCOL * (D + 4);
             int node = r0 / p.group, hd = r0 % p.group;
 #pragma unroll 1
             for (int cb = 0; cb < NCOL; cb += 16) {
@@ -426,10 +425,10 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                             static_cast<__nv_bfloat16*>(p.out)[((size_t)(n0 + node) * p.Hq + kvh * p.group + hd) * D + key] =
                                 __float2bfloat16_rn(__fdividef(val, sum));
                         else
-                            part[(size_t)c * (D + 2) + key] = val;
+                            part[(size_t)c * (D + 4) + key] = val;
                     }
                     if (!whole && key < 2)
-                        part[(size_t)c * (D + 2) + D + key] = key == 0 ? (nref[c] == -kNoRef ? -INFINITY : -nref[c]) : sum;
+                        part[(size_t)c * (D + 4) + D + key] = key == 0 ? (nref[c] == -kNoRef ? -INFINITY : -nref[c]) : sum;
                     if (++hd == p.group) {
                         hd = 0;
                         ++node;

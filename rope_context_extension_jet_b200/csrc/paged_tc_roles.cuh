@@ -34,8 +34,8 @@ struct UnitDesc {
     int L, T, n0, b;     // committed rows, nodes, first token row, request
     int kvh, r0;         // kv head, first query row
     int i0, i1;          // its items in this piece
-    int gmin, ng, nR, kE0, w0, items;
-    int pad;
+    int gmin, ng, nR, kE0, w0, items, pad0;
+    unsigned long long bad;  // drafted nodes whose value rows hold infinities or NaN (value producer)
 };
 typedef const volatile UnitDesc* UnitPtr;
 
@@ -56,18 +56,23 @@ template <int D, int ROWS, int NSK, int NSV, int BASE, int EXTRA_BARS, int WARPS
 struct Notes {
     static constexpr int UNIT = BASE;
     static constexpr int U_ANC = 0, U_DEPTH = U_ANC + ROWS * 8, U_LIM = U_DEPTH + kMaxNodes * 4, U_QG = U_LIM + ROWS * 4;
-    static constexpr int U_CQ = U_QG + ROWS * 4, U_BAD = U_CQ + ROWS * 4, UBYTES = U_BAD + 16;
+    static constexpr int U_CQ = U_QG + ROWS * 4, U_BIG = U_CQ + ROWS * 4, UBYTES = U_BIG + 16;
     static constexpr int QS = UNIT + 2 * UBYTES;            // [ROWS] query scales
     static constexpr int PAR = QS + ROWS * 4;               // [64] parents, [64] node ancestors
     static constexpr int KSC = PAR + kMaxNodes * 12;        // [INFO][128] inverse key scales
     static constexpr int TURNS = KSC + INFO * KT * 4;       // [D / 2] phase constants (hi, lo)
     static constexpr int NOTE = TURNS + D / 2 * 8;          // [INFO] mask of the pages present
-    static constexpr int SCALED = NOTE + INFO * 4;          // [INFO][4] a rotation warp scaled rows of the tile
-    static constexpr int PLAN = SCALED + INFO * 16;
+    static constexpr int SCALED = NOTE + INFO * 4;          // [INFO][8] a rotation warp scaled rows of the tile
+    static constexpr int PLAN = SCALED + INFO * 32;
     static constexpr int DESC = PLAN + (int)sizeof(PiecePlan);
     static constexpr int SCAN = DESC + UNITS * (int)sizeof(UnitDesc);
     static constexpr int BAR = SCAN + (WARPS + 1) * 8;
-    static constexpr int NBARS = 3 * NSK + 3 * NSV + 5 + 1 + 2 * UNITS + EXTRA_BARS;
+    // Landed key tiles are announced on a ring of an even number of barriers, apart
+    // from the ring of stages: the two rotation warpgroups wait for every second tile,
+    // and a barrier that one of them sees only every second time around would let a
+    // parity wait pass a phase early.
+    static constexpr int NKF = NSK + (NSK & 1);
+    static constexpr int NBARS = NKF + 2 * NSK + 3 * NSV + 5 + 1 + 2 * UNITS + EXTRA_BARS;
     static constexpr int SLOT = BAR + NBARS * 8;            // TMEM address, abort flag
     static constexpr int NOTES_END = (SLOT + 16 + 15) / 16 * 16;
     static_assert(INFO > NSK + 1, "ring of per-item notes");
@@ -94,7 +99,7 @@ struct Bars {
     __device__ __forceinline__ Bars()
     {
         kfull = reinterpret_cast<uint64_t*>(smem_base() + C::BAR);
-        kready = kfull + C::NSK;
+        kready = kfull + C::NKF;
         kempty = kready + C::NSK;
         vfull = kempty + C::NSK;
         vfix = vfull + C::NSV;
@@ -110,14 +115,14 @@ struct Bars {
     // one thread; C::ROT threads rotate a tile, C::ROTALL in all, C::SOFT softmax warps
     __device__ __forceinline__ void init()
     {
+        for (int s = 0; s < C::NKF; ++s) mbar_init(&kfull[s], 1);
         for (int s = 0; s < C::NSK; ++s) {
-            mbar_init(&kfull[s], 1);
             mbar_init(&kready[s], C::ROT / 32);
             mbar_init(&kempty[s], 1);
         }
         for (int s = 0; s < C::NSV; ++s) {
             mbar_init(&vfull[s], 1);
-            mbar_init(&vfix[s], C::ROT / 32);
+            mbar_init(&vfix[s], 1);
             mbar_init(&vempty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -287,7 +292,8 @@ __device__ __forceinline__ uint32_t start_cta(const Role<C>& ro, InitExtra init_
 }
 
 // Producer of key tiles (warp 0) or value tiles (warp 3): the page numbers of a
-// tile's rows, then one TMA box per page and 64 columns.
+// tile's rows, then one TMA box per page and 64 columns.  The value producer also
+// clears what a request's last tile must not hold.
 template <class C, bool isK>
 __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm)
 {
@@ -297,22 +303,24 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
     const Bars<C> bars;
     const int lane = ro.lane;
     constexpr int D = C::DIM;
-        constexpr int NS = isK ? C::NSK : C::NSV;
+    constexpr int NS = isK ? C::NSK : C::NSV;
+    constexpr int NF = isK ? C::NKF : C::NSV;  // barriers of landed tiles
     uint64_t* full = isK ? bars.kfull : bars.vfull;
     uint64_t* empty = isK ? bars.kempty : bars.vempty;
-        unsigned char* ring = smem + (isK ? C::K0 : C::V0);
-    const int box = min(p.page_size, KT);
+    unsigned char* ring = smem + (isK ? C::K0 : C::V0);
+    const int box = min(p.page_size, KT), gshift = min(p.page_shift, 7);
+    const unsigned all_pages = ro.all_pages();
     int e = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-        if (!ro.unit_wait(k, 0x403)) break;
+        if (!ro.unit_wait(k, isK ? 0x403 : 0x404)) break;
         UnitPtr un = ro.unit(k);
         if (un->rows == 0) break;
         const int* table = p.table + (size_t)un->b * p.max_pages;
-        const int n = un->L + un->T, kvh = un->kvh;
+        const int L = un->L, n = L + un->T, kvh = un->kvh;
         for (UnitItems it(un); it.left > 0; it.next(), ++e) {
             // lane x looks after rows [x box, (x + 1) box) of the tile
-            const int row = it.tile * KT + lane * box;
+            const int j0 = it.tile * KT, row = j0 + lane * box;
             const bool want = lane * box < KT && row < n;
             int page = -1;
             if (want) {
@@ -330,9 +338,9 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
                 if (isK) ro.note()[e % INFO] = have;
                 if (!skip) {
                     if (have)
-                        mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(have) * box * D * 2));
+                        mbar_arrive_expect_tx(&full[e % NF], (uint32_t)(__popc(have) * box * D * 2));
                     else
-                        mbar_arrive(&full[st]);
+                        mbar_arrive(&full[e % NF]);
                 }
             }
             __syncwarp();
@@ -340,14 +348,55 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
                 unsigned char* dst = ring + st * C::TILE + lane * box * 128;
                 const int y = row & (p.page_size - 1), z = page * p.Hkv + kvh;
 #pragma unroll
-                for (int a = 0; a < C::ATOMS; ++a) tma_load_3d(dst + a * C::ATOM_K, tm, a * 64, y, z, &full[st]);
+                for (int a = 0; a < C::ATOMS; ++a) tma_load_3d(dst + a * C::ATOM_K, tm, a * 64, y, z, &full[e % NF]);
+            }
+            if (!isK && (j0 + KT > L || have != all_pages)) {
+                // Value rows that do not exist count as zero: the page may hold anything
+                // there, and a weight of 0 does not silence NaN.  A drafted row's own
+                // infinities and NaN are cleared as well (nodes beside it must not see
+                // them) and noted for the nodes that do attend it.
+                if (!ro.wait(&full[e % NF], (e / NF) & 1, 0x405)) {
+                    ++e;  // its copy is in flight
+                    ok = false;
+                    break;
+                }
+                unsigned char* vt = ring + st * C::TILE;
+                const int first = have == all_pages ? max(0, L - j0) : 0;
+                for (int r = first + lane; r < KT; r += 32) {
+                    const int j = j0 + r;
+                    const bool there = j < n && ((have >> (r >> gshift)) & 1);
+                    if (there && j < L) continue;
+                    bool hit = false;
+#pragma unroll 4
+                    for (int x = 0; x < D / 8; ++x) {
+                        uint4* v = reinterpret_cast<uint4*>(vt + tc::sw128_off<KT>(r, x));
+                        if (!there) {
+                            *v = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint4 w = *v;
+                        uint32_t* y = &w.x;
+                        bool any = false;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if ((y[u] & 0x7f80u) == 0x7f80u) { y[u] &= 0xffff0000u; any = true; }
+                            if ((y[u] & 0x7f800000u) == 0x7f800000u) { y[u] &= 0xffffu; any = true; }
+                        }
+                        if (any) *v = w;
+                        hit |= any;
+                    }
+                    if (hit) atomicOr(const_cast<unsigned long long*>(&un->bad), 1ull << (j - L));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.vfix[st]);
             }
         }
         ro.unit_done(k);
     }
     // the copies in flight land before the CTA ends
     for (int x = max(0, e - NS); x < e; ++x)
-        if (!(isK && x == 0 && ln.inject == kInjectDecodeCopy)) mbar_wait(&full[x % NS], (x / NS) & 1);
+        if (!(isK && x == 0 && ln.inject == kInjectDecodeCopy)) mbar_wait(&full[x % NF], (x / NF) & 1);
 }
 
 // Planner (one thread of warp 2): the units of this CTA's piece, a few ahead.
@@ -366,6 +415,7 @@ __device__ __forceinline__ void plan_units(const Role<C>& ro)
         for (;; ++k) {
             UnitDesc u;
             u.rows = 0;
+            u.bad = 0;
             if (cur < end) {
                 long long cnt = (long long)s.items * s.row_tiles * p.Hkv;
                 while (cur >= base + cnt) {
@@ -405,8 +455,7 @@ __device__ __forceinline__ void plan_units(const Role<C>& ro)
 
 // Rotation (C::ROTALL threads from thread 128 on).  Per unit: the tree, positions and
 // query scales.  Per phase: the queries rotated into shared memory.  Per tile: the
-// keys rotated in place; on a request's last tiles the value rows that do not exist
-// are cleared.
+// keys rotated in place.
 template <class C>
 __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
 {
@@ -414,9 +463,9 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
     unsigned char* const smem = smem_base();
     const Bars<C> bars;
     const int lane = ro.lane;
-    constexpr int D = C::DIM, H = D / 2, CH = D / 16, NSK = C::NSK, NSV = C::NSV;
+    constexpr int D = C::DIM, H = D / 2, CH = D / 16, NSK = C::NSK;
     float* ksc = reinterpret_cast<float*>(smem + C::KSC);
-        const int t = (int)threadIdx.x - 128, rt = t & (C::ROT - 1);  // thread of the role, of the tile
+    const int t = (int)threadIdx.x - 128, rt = t & (C::ROT - 1);  // thread of the role, of the tile
     const int group = C::ALT ? t >> 7 : 0;
     constexpr int RPT = KT * CH / C::ROT;          // rows per thread of a tile: 128 rows x CH chunk pairs
     const int c = t % CH, row0 = (rt / CH) * RPT;
@@ -470,8 +519,6 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
         a.z = pack_bf16x2(bf16_lo(a.z) * sc, bf16_hi(a.z) * sc);
         a.w = pack_bf16x2(bf16_lo(a.w) * sc, bf16_hi(a.w) * sc);
     };
-    const int gshift = min(p.page_shift, 7);
-    const unsigned all_pages = (1u << (KT >> gshift)) - 1;
     int* par = reinterpret_cast<int*>(smem + C::PAR);
     unsigned long long* nanc = reinterpret_cast<unsigned long long*>(par + kMaxNodes);
     float* qsc = reinterpret_cast<float*>(smem + C::QS);
@@ -490,10 +537,10 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
         int* qG = reinterpret_cast<int*>(un + C::U_QG);
         float* cq = reinterpret_cast<float*>(un + C::U_CQ);
         unsigned long long* canc = reinterpret_cast<unsigned long long*>(un + C::U_ANC);
-        unsigned long long* bad = reinterpret_cast<unsigned long long*>(un + C::U_BAD);
-        int* big = reinterpret_cast<int*>(bad + 1);
-        // the softmax is done with unit nu - 2, the tensor cores with the
-        // queries of unit nu - 1
+        int* big = reinterpret_cast<int*>(un + C::U_BIG);
+        // the softmax is done with unit nu - 2, the tensor cores with the queries of
+        // unit nu - 1 (known to the warps that rotated item e - 1, and through the
+        // barrier to the others)
         ok = ok && (nu < 2 || ro.wait(&bars.ufree[nu & 1], ((nu >> 1) - 1) & 1, 0x421)) &&
              (e == 0 || ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x422));
         if ((agreed = named_or(1, C::ROTALL, !ok))) break;
@@ -509,10 +556,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             }
             par[t] = x;
         }
-        if (t == 0) {
-            *bad = 0;
-            *big = 0;
-        }
+        if (t == 0) *big = 0;
         named_sync(1, C::ROTALL);
         if (t < T) {
             unsigned long long m = (2ull << t) - 1;
@@ -524,60 +568,74 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             depth[t] = __popcll(m) - 1;
         }
         named_sync(1, C::ROTALL);
-        // The unit's queries turned for the phase of group size g, as fp16.  CH threads
-        // share a row.  The first time also the row's notes: each query is multiplied by
-        // a power of two that brings its largest element into [2^13, 2^14), its logits
-        // by the inverse.
+        // The unit's queries turned for the phase of group size g, as fp16.  A task is a
+        // chunk of `span` heads of one node, which share their angles: one head where that
+        // gives every thread at most one task.  The first time also the rows' notes: each
+        // query is multiplied by a power of two that brings its largest element into
+        // [2^13, 2^14), its logits by the inverse.
+        const int node0 = r0 / p.group, nodes = (r0 + rows - 1) / p.group - node0 + 1;
+        const int span = rows * CH <= C::ROTALL ? 1 : min(p.group, (rows * CH + C::ROTALL - 1) / C::ROTALL);
+        const int spans = (p.group + span - 1) / span;
         auto queries = [&](int g, bool setup) {
-            const uint32_t dv = max(g, 1);
-#pragma unroll 2
-            for (int x = t; x < C::ROWS * CH; x += C::ROTALL) {
-                const int row = x / CH;  // CH divides the thread count: chunk x % CH = c
-                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                int pos = 0;
-                float sc = 0.f;
-                if (row < rows) {
-                    const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
-                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)(n0 + node) * p.Hq + hd) * D;
-                    lo = *reinterpret_cast<const uint4*>(q + c * 8);
-                    hi = *reinterpret_cast<const uint4*>(q + H + c * 8);
-                    pos = L + depth[node];
-                }
-                if (setup) {
-                    uint32_t mx = mag16(absmax8(lo, hi));
-                    float l1 = sum8(lo) + sum8(hi);
-#pragma unroll
-                    for (int o = 1; o < CH; o <<= 1) {
-                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-                    }
-                    const int ex = tc::range_exp(mx);
-                    sc = tc::pow2i(ex);
-                    if (c == 0) {
-                        // a normal number: -inf times it stays -inf
-                        const float inv = fminf(fmaxf(tc::pow2i(-ex) * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);
-                        lim0[row] = pos - ud->w0;
-                        qG[row] = row < rows ? pos / p.w_pre + 1 : 0;
-                        canc[row] = row < rows ? nanc[(r0 + row) / p.group] : 0ull;
-                        cq[row] = row < rows ? inv : 0.f;
-                        qsc[row] = sc;
-                        // keys rounded to fp16 as they are err by up to 2^-25 where fp16 is
-                        // subnormal; with an L1 norm this large that could reach 2^-11 of a logit
-                        if (!(l1 * p.scale_log2 * 1.4142136f <= 16384.f)) *big = 1;
-                    }
-                } else {
-                    sc = qsc[row];
-                }
+            const int tasks = nodes * spans * CH, end = (tasks + 31) / 32 * 32;  // whole warps
+#pragma unroll 1
+            for (int x = t; x < end; x += C::ROTALL) {  // CH divides the thread count: chunk x % CH = c
+                const int y = x / CH, node = min(node0 + y / spans, T - 1), h0 = (y % spans) * span;
+                const int pos = L + depth[node];
                 Angles by;
-                angles((uint32_t)pos / dv, by);
+                angles((uint32_t)pos / (uint32_t)max(g, 1), by);
+#pragma unroll 1
+                for (int h = h0; h < h0 + span; ++h) {
+                    const int row = node * p.group + h - r0;
+                    const bool live = x < tasks && h < p.group && row >= 0 && row < rows;
+                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                    if (live) {
+                        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
+                                                 ((size_t)(n0 + node) * p.Hq + kvh * p.group + h) * D + c * 8;
+                        lo = *reinterpret_cast<const uint4*>(q);
+                        hi = *reinterpret_cast<const uint4*>(q + H);
+                    }
+                    float sc;
+                    if (setup) {
+                        uint32_t mx = mag16(absmax8(lo, hi));
+                        float l1 = sum8(lo) + sum8(hi);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    by.cs[u] = make_float2(by.cs[u].x * sc, by.cs[u].y * sc);
-                    by.sn[u] = make_float2(by.sn[u].x * sc, by.sn[u].y * sc);
+                        for (int o = 1; o < CH; o <<= 1) {
+                            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+                        }
+                        const int ex = tc::range_exp(mx);
+                        sc = tc::pow2i(ex);
+                        if (c == 0 && live) {
+                            lim0[row] = pos - ud->w0;
+                            qG[row] = pos / p.w_pre + 1;
+                            canc[row] = nanc[node];
+                            // a normal number: -inf times it stays -inf
+                            cq[row] = fminf(fmaxf(tc::pow2i(-ex) * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);
+                            qsc[row] = sc;
+                            // keys rounded to fp16 as they are err by up to 2^-25 where fp16 is
+                            // subnormal; with an L1 norm this large that could reach 2^-11 of a logit
+                            if (!(l1 * p.scale_log2 * 1.4142136f <= 16384.f)) *big = 1;
+                        }
+                    } else {
+                        sc = live ? qsc[row] : 1.f;
+                    }
+                    if (live) {
+                        scale8(lo, sc);
+                        scale8(hi, sc);
+                        turn(lo, hi, by);
+                        *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c)) = lo;
+                        *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c + CH)) = hi;
+                    }
                 }
-                turn(lo, hi, by);
-                *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c)) = lo;
-                *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c + CH)) = hi;
+            }
+            if (setup) {
+                // rows without a query: logits times 0 whatever the tile holds, nothing attended
+                for (int row = rows + t; row < C::ROWS; row += C::ROTALL) {
+                    lim0[row] = qG[row] = 0;
+                    canc[row] = 0ull;
+                    cq[row] = 0.f;
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -601,7 +659,13 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
         for (; it.left > 0; it.next(), ++e) {
             if (it.g != gcur) {
                 // the next phase; the tensor cores are done with the queries of the last
-                if (!ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423)) { ok = false; break; }
+                // (only the warps that rotated item e - 1 know that the wait is for its phase:
+                // the others follow through the barrier)
+                ok = ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423);
+                if ((agreed = named_or(1, C::ROTALL, !ok))) {
+                    ok = false;
+                    break;
+                }
                 gcur = it.g;
                 set_divisor(gcur);
                 queries(gcur, false);
@@ -638,7 +702,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                 // with four rows per turn the 128K batch took 1130 us instead of 810.)
                 uint32_t f = over_g((uint32_t)(j0 + row0));
                 angles(f, by);
-                if (!ro.wait(&bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
+                if (!ro.wait(&bars.kfull[e % C::NKF], (e / C::NKF) & 1, 0x424)) { ok = false; break; }
                 auto advance = [&](int r) {
                     const uint32_t fn = over_g((uint32_t)(j0 + r));
                     if (fn != f) {
@@ -677,7 +741,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             } else {
                 // a request's last tiles: drafted rows sit at their depths (rows past the
                 // end: 0, they are masked)
-                if (!ro.wait(&bars.kfull[st], (e / NSK) & 1, 0x424)) { ok = false; break; }
+                if (!ro.wait(&bars.kfull[e % C::NKF], (e / C::NKF) & 1, 0x424)) { ok = false; break; }
 #pragma unroll 1
                 for (int x = 0; x < RPT; ++x) {
                     const int r = row0 + x, j = j0 + r;
@@ -693,48 +757,10 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                     *pb = b;
                 }
             }
-            if (lane == 0) reinterpret_cast<volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 4 + (rt >> 5)] = scaled;
+            if (lane == 0) reinterpret_cast<volatile unsigned*>(smem + C::SCALED)[(e % INFO) * 8 + (rt >> 5)] = scaled;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.kready[st]);
-            // value rows that do not exist count as zero: the page may hold
-            // anything there, and a weight of 0 does not silence NaN.  A drafted
-            // row's own infinities and NaN are cleared as well (nodes beside it
-            // must not see them) and noted for the nodes that do attend it.
-            const unsigned have = ro.note()[e % INFO];
-            if (drafted || have != all_pages) {
-                const int sv = e % NSV;
-                if (!ro.wait(&bars.vfull[sv], (e / NSV) & 1, 0x425)) { ok = false; break; }
-                unsigned char* vt = smem + C::V0 + sv * C::TILE;
-                constexpr int TPR = C::ROT / KT;  // threads per row
-                const int r = rt / TPR, j = j0 + r;
-                const bool there = j < n && ((have >> (r >> gshift)) & 1);
-                if (!there || j >= L) {
-#pragma unroll 1
-                    for (int k = rt % TPR; k < D / 8; k += TPR) {
-                        uint4* v = reinterpret_cast<uint4*>(vt + tc::sw128_off<KT>(r, k));
-                        if (!there) {
-                            *v = make_uint4(0u, 0u, 0u, 0u);
-                            continue;
-                        }
-                        uint4 x = *v;
-                        uint32_t* y = &x.x;
-                        bool hit = false;
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if ((y[u] & 0x7f80u) == 0x7f80u) { y[u] &= 0xffff0000u; hit = true; }
-                            if ((y[u] & 0x7f800000u) == 0x7f800000u) { y[u] &= 0xffffu; hit = true; }
-                        }
-                        if (hit) {
-                            *v = x;
-                            atomicOr(bad, 1ull << (j - L));
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.vfix[sv]);
-            }
         }
         ro.unit_done(nu);
     }
