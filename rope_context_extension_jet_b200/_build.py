@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libjetlong.so")
 
 SOURCES = ["jetlong_api.cu", "position_map.cu", "range_scan.cu", "rope_keys.cu", "prefill_simt.cu", "prefill_tc.cu",
            "prefill_pair.cu", "ie_merge.cu", "decode.cu", "debug_kernels.cu", "paged_tables.cu", "paged_rows.cu",
-           "decode_paged.cu", "decode_paged_tc.cu", "decode_paged_rows.cu"]
+           "decode_paged.cu", "decode_paged_fp32.cu", "decode_paged_tc.cu", "decode_paged_rows.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC] + ARCH

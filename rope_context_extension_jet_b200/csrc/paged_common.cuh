@@ -99,6 +99,9 @@ cudaError_t launch_tree_commit(const CommitProblem& p, cudaStream_t s, int* nlau
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int d, int max_nodes);
 int paged_tc_rows(int rows);
 size_t paged_tc_workspace(int rows, int d);
+int paged_fp32_rows(int rows);
+size_t paged_fp32_workspace(int rows, int d);
+cudaError_t launch_decode_paged_fp32(const PagedProblem& p, int d, cudaStream_t s, int* grid);
 cudaError_t launch_decode_paged_tc(const PagedProblem& p, int d, cudaStream_t s, int* grid);
 cudaError_t launch_decode_paged(const PagedProblem& p, int d, jetlong_dtype dt, cudaStream_t s, int* nlaunch);
 
@@ -294,32 +297,6 @@ __device__ __forceinline__ void note_cut(const PagedProblem& p, const SeqPlan& s
     c->r0 = r0;
 }
 
-// The items of a unit in order: the group size its keys are aliased by (0: exact
-// positions) and the key tile.
-struct Items {
-    int g, tile;
-    __device__ __forceinline__ void start(const SeqPlan& s, int i)
-    {
-        const int rem = s.ng * s.nR;
-        if (i < rem) {
-            g = s.gmin + i / s.nR;
-            tile = i % s.nR;
-        } else {
-            g = 0;
-            tile = s.kE0 + (i - rem);
-        }
-    }
-    __device__ __forceinline__ void next(const SeqPlan& s)
-    {
-        ++tile;
-        if (g != 0 && tile == s.nR) {
-            const bool more = g + 1 < s.gmin + s.ng;
-            tile = more ? 0 : s.kE0;
-            g = more ? g + 1 : 0;
-        }
-    }
-};
-
 // Quotient and remainder of a unit's place by its items; 64-bit division only
 // where it is needed.
 __device__ __forceinline__ void div_items(long long x, int items, int* q, int* r)
@@ -331,37 +308,6 @@ __device__ __forceinline__ void div_items(long long x, int items, int* q, int* r
         *q = (int)(x / items);
         *r = (int)(x % items);
     }
-}
-
-// Depth and ancestors-or-self of the T nodes of a request, by threads
-// 0 .. kMaxNodes - 1; par is shared scratch.  A parent that does not precede
-// its node counts as -1.
-__device__ inline void load_tree(const PagedProblem& p, const SeqPlan& s, int* par, int* depth, unsigned long long* anc)
-{
-    const int t = threadIdx.x;
-    if (t < s.T) {
-        int x = t - 1;
-        if (p.parents) {
-            x = p.parents[s.n0 + t];
-            if (x < -1 || x >= t) {
-                record_input(p.input_error, kBadParent);
-                x = -1;
-            }
-        }
-        par[t] = x;
-    }
-    __syncthreads();
-    if (t < s.T) {
-        unsigned long long m = 0;
-        if (p.parents) {
-            for (int x = t; x >= 0; x = par[x]) m |= 1ull << x;
-        } else {
-            m = (2ull << t) - 1;  // t = 63: 2 << 63 is 0, so all ones
-        }
-        anc[t] = m;
-        depth[t] = __popcll(m) - 1;
-    }
-    __syncthreads();
 }
 
 #endif  // __CUDACC__

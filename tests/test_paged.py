@@ -152,8 +152,9 @@ def test_long_and_short_requests_cut_into_pieces(dtype):
     check_tree(17, [6000, 3, 2500, 0, 4097], [1, 4, 2, 3, 6], w_pre=1000, w0=300, dtype=dtype)
 
 
-@pytest.mark.parametrize("d,nodes", [(128, 1), (128, 4), (128, 8), (128, 16), (128, 40), (64, 1), (64, 8), (64, 16), (64, 40)])
-def test_long_batches_keep_their_tiles_apart(d, nodes):
+@pytest.mark.parametrize("d,nodes,dtype", [(d, t, "bf16") for d in (128, 64) for t in (1, 4, 8, 16, 40)] +
+                         [(d, t, "fp32") for d in (128, 64) for t in (1, 2, 4, 10)])
+def test_long_batches_keep_their_tiles_apart(d, nodes, dtype):
     """Every CTA works through dozens of tiles, several units and phases with its
     rings of tiles always full; runs repeat bit for bit.  Rows no request owns hold
     NaN, so that a tile taken too early or repaired too late shows."""
@@ -164,14 +165,14 @@ def test_long_batches_keep_their_tiles_apart(d, nodes):
     gen = torch.Generator(device="cuda").manual_seed(5)
     num = B * pages + 1
     table = torch.randperm(num, generator=gen, device="cuda")[:B * pages].view(B, pages).int()
-    kc, vc = (torch.randn(num, Hkv, ps, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    kc, vc = (torch.randn(num, Hkv, ps, d, generator=gen, device="cuda").to(dt(dtype)) for _ in range(2))
     for b, L in enumerate(lens):
         n = L + nodes
         for c in (kc, vc):
             c[table[b, -(-n // ps):].long()] = float("nan")
             if n % ps:
                 c[int(table[b, n // ps]), :, n % ps:] = float("nan")
-    q = queries(5, B * nodes, Hq, d, "bf16")
+    q = queries(5, B * nodes, Hq, d, dtype)
     par = random_parents(np.random.default_rng(5), nodes, "comb")
     args = (q, kc, vc, table, ints(lens), ints([b * nodes for b in range(B + 1)]), ints(par * B))
     kw = dict(max_nodes=nodes, w0=700, w_pretrained=5000, rope_theta=1e6)
@@ -179,7 +180,7 @@ def test_long_batches_keep_their_tiles_apart(d, nodes):
     jl.device_status()
     for _ in range(20):
         again = jl.decode_tree(*args, **kw)
-        assert torch.equal(again.view(torch.int16), got.view(torch.int16))
+        assert torch.equal(again.view(torch.int16), got.view(torch.int16))  # (bits: no NaN may hide)
     jl.device_status()
     got, q64, tab = to64(got), to64(q), table.cpu().numpy()
     for b, L in enumerate(lens):
@@ -188,7 +189,7 @@ def test_long_batches_keep_their_tiles_apart(d, nodes):
         k1, v1 = (torch.zeros(pages, 1, ps, d) for _ in range(2))
         k1[:, 0], v1[:, 0] = (c[table[b].long(), h].float().cpu() for c in (kc, vc))
         ref, tol = R.attend(q64[rows, heads], k1.numpy().astype(np.float64), v1.numpy().astype(np.float64), np.arange(pages), L,
-                            par, w0=700, w_pre=5000, theta=1e6, scale=d ** -0.5, dtype="bf16")
+                            par, w0=700, w_pre=5000, theta=1e6, scale=d ** -0.5, dtype=dtype)
         err = np.abs(got[rows, heads] - ref)
         assert (err <= tol).all(), (b, L, float((err / tol).max()))
 
