@@ -7,8 +7,9 @@
 // warps compute.  LPK lanes share a key, each with 4 + 4 of its dimensions (the two
 // halves of 4 rotation pairs) of R query rows in registers, so a key is read from
 // shared memory once per R rows:
-//   rotation   4 pairs in registers; angles fresh every 8 keys, between them by
-//              angle addition (at most 7 steps of 3 * 2^-24 each)
+//   rotation   4 pairs in registers; angles fresh for each run of 8 or 16 keys, inside it
+//              by angle addition (at most 15 steps of 3 * 2^-24 each: below half of
+//              what the products' 128 terms may round by)
 //   logits     partial dots of KB = LPK / R keys, then a halving exchange that leaves
 //              one (key, row) logit on each lane
 //   softmax    the lane's running reference, moved only when a logit passes it by
@@ -32,7 +33,7 @@ constexpr int CW = 8, CT = CW * 32;     // computing warps, threads
 constexpr int NTHR = CT + 128;          // and the producer's warpgroup
 // Registers per thread after setmaxnreg: the two computing warpgroups, the producer's
 // (384 threads launch with 168 each, and an increase draws on that).
-constexpr int R_CALC = 224, R_PROD = 40;
+constexpr int R_CALC = 232, R_PROD = 40;
 static_assert((2 * R_CALC + R_PROD) * 128 <= NTHR * 168, "register split");
 constexpr int kCtas = 148;              // one per SM
 constexpr int kMinItems = 4;            // tiles of a piece at least
@@ -325,20 +326,18 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
                 const int jr = j0 + grp * C::RUN;
                 uint32_t f = 0;
                 float2 cs[2], sn[2];
-#pragma unroll 1
-                for (int kk = 0; kk < C::RUN; kk += KB) {
+                // Logit `sub` of the batch of keys from kk on: key kk + sub / R, row sub % R.
+                // Within a run the turned position of row j, floor(j / g), stays or steps by one.
+                auto logit = [&](int kk, bool fresh) {
                     float acc[LPK];
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
                         const int j = jr + kk + b;
-                        if (risky) {
-                            const uint32_t pos = j < L ? (uint32_t)j : j < n ? (uint32_t)(L + depth[j - L]) : 0u;
-                            angles(over_g(pos), cs, sn);
+                        if (fresh) {
+                            angles(over_g(j < L ? (uint32_t)j : j < n ? (uint32_t)(L + depth[j - L]) : 0u), cs, sn);
                         } else {
                             const uint32_t fn = over_g((uint32_t)j);
-                            if (b == 0 && kk % 8 == 0) {
-                                angles(fn, cs, sn);
-                            } else if (fn != f) {  // one position further
+                            if (fn != f) {
 #pragma unroll
                                 for (int u = 0; u < 2; ++u) {
                                     const float2 nc = fma2(make_float2(-sn[u].x, -sn[u].y), sts[u], mul2(cs[u], stc[u]));
@@ -362,7 +361,6 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
                             acc[b * R + r] = d.x + d.y;
                         }
                     }
-                    // lane `sub` ends with logit sub: key kk + sub / R, row sub % R
 #pragma unroll
                     for (int w = LPK / 2; w >= 1; w >>= 1) {
                         const bool hi = lane & w;
@@ -372,7 +370,10 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
                             acc[u] = mine + __shfl_xor_sync(0xffffffffu, give, w);
                         }
                     }
-                    float y = acc[0];
+                    return acc[0];
+                };
+                // its weight; the reference moves where it has to
+                auto weight = [&](float y, int kk) {
                     if (masked) {
                         const int kx = grp * C::RUN + kk + sub / R, j = j0 + kx, u = j - L;
                         const bool there = j < n && ((have >> (kx >> shift)) & 1) && row < nrows;
@@ -401,6 +402,9 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
                     }
                     const float w = exp2f(y - (ref == -INFINITY ? 0.f : ref));
                     l += w;
+                    return w;
+                };
+                auto values = [&](float w, int kk, bool guard) {
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
                         const float4 a = *reinterpret_cast<const float4*>(vt + (kk + b) * D);
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             const float wr = __shfl_sync(0xffffffffu, w, b * R + r, LPK);
-                            if (!risky || wr != 0.f) {
+                            if (!guard || wr != 0.f) {
                                 const float2 w2 = make_float2(wr, wr);
                                 o[r][0] = fma2(w2, make_float2(a.x, a.y), o[r][0]);
                                 o[r][1] = fma2(w2, make_float2(a.z, a.w), o[r][1]);
@@ -417,6 +421,23 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
                             }
                         }
                     }
+                };
+                if (!risky) {
+                    // the next batch's logits beside this one's values: the exchanges wait on
+                    // shuffles that the values' arithmetic hides
+                    f = over_g((uint32_t)jr);
+                    angles(f, cs, sn);
+                    float y = logit(0, false);
+#pragma unroll 1
+                    for (int kk = 0; kk < C::RUN - KB; kk += KB) {
+                        const float w = weight(y, kk);
+                        y = logit(kk + KB, false);
+                        values(w, kk, false);
+                    }
+                    values(weight(y, C::RUN - KB), C::RUN - KB, false);
+                } else {
+#pragma unroll 1
+                    for (int kk = 0; kk < C::RUN; kk += KB) values(weight(logit(kk, true), kk), kk, true);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);
