@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::FLAG);
     PiecePlan* plan = reinterpret_cast<PiecePlan*>(smem + C::PLAN);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
+    if (tid == NTHR - 1) {  // (the first threads go on to the requests' lengths)
         for (int s = 0; s < C::NB; ++s) mbar_init(&full[s], 1);
         for (int s = 0; s < C::NS; ++s) mbar_init(&empty[s], C::WR);
         // an earlier wait ran out: no work

@@ -396,8 +396,16 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             const unsigned long long bad = ud->bad;
             float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
                           ((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NCOL * (D + 4);
-            int node = r0 / p.group, hd = r0 % p.group;
-#pragma unroll 1
+            // lane c looks after column c: its sum and where its row goes
+            const int node0 = r0 / p.group, mine = min(lane, cols - 1);
+            const float sum = red[mine] + red[NCOL + mine] + red[2 * NCOL + mine] + red[3 * NCOL + mine];
+            const float inv = whole ? __fdividef(1.f, sum) : 1.f;
+            const int to = whole ? ((r0 + mine) / p.group - node0) * p.Hq + (r0 + mine) % p.group : mine;
+            __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + ((size_t)(n0 + node0) * p.Hq + kvh * p.group) * D + key;
+            if (!whole && wl == 0 && lane < cols)
+                *reinterpret_cast<float2*>(part + lane * (D + 4) + D) =
+                    make_float2(nref[lane] == -kNoRef ? -INFINITY : -nref[lane], sum);
+#pragma unroll
             for (int cb = 0; cb < NCOL; cb += 16) {
                 if (cb >= cols) break;
                 uint32_t o[16];
@@ -405,33 +413,32 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 tmem_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    const int c = cb + x;
-                    if (c >= cols) break;
-                    float val = __uint_as_float(o[x]);
-                    const float sum = red[c] + red[NCOL + c] + red[2 * NCOL + c] + red[3 * NCOL + c];
-                    if (bad && key < D) {
-                        asm volatile("" ::: "memory");
-                        // infinities and NaN of drafted rows this node attends
-                        for (unsigned long long rest = bad & canc[c]; rest; rest &= rest - 1) {
-                            const int row = L + __ffsll((long long)rest) - 1;
-                            const int page = p.table[(size_t)ud->b * p.max_pages + (row >> p.page_shift)];
-                            const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.vc)[
-                                (((size_t)page * p.Hkv + kvh) * p.page_size + (row & (p.page_size - 1))) * D + key]);
-                            if (!(fabsf(v) < INFINITY)) val += v;
-                        }
-                    }
-                    if (key < D) {
+                    const int row = __shfl_sync(0xffffffffu, to, cb + x);
+                    const float val = __uint_as_float(o[x]) * __shfl_sync(0xffffffffu, inv, cb + x);
+                    if (key < D && cb + x < cols) {
                         if (whole)
-                            static_cast<__nv_bfloat16*>(p.out)[((size_t)(n0 + node) * p.Hq + kvh * p.group + hd) * D + key] =
-                                __float2bfloat16_rn(__fdividef(val, sum));
+                            orow[(size_t)row * D] = __float2bfloat16_rn(val);
                         else
-                            part[(size_t)c * (D + 4) + key] = val;
+                            part[row * (D + 4) + key] = val;
                     }
-                    if (!whole && key < 2)
-                        part[(size_t)c * (D + 4) + D + key] = key == 0 ? (nref[c] == -kNoRef ? -INFINITY : -nref[c]) : sum;
-                    if (++hd == p.group) {
-                        hd = 0;
-                        ++node;
+                }
+            }
+            if (bad && key < D) {
+                // infinities and NaN of drafted rows a node attends: they outweigh what this
+                // thread has just written
+                for (int c = 0; c < cols; ++c) {
+                    for (unsigned long long rest = bad & canc[c]; rest; rest &= rest - 1) {
+                        const int row = L + __ffsll((long long)rest) - 1;
+                        const int page = p.table[(size_t)ud->b * p.max_pages + (row >> p.page_shift)];
+                        const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.vc)[
+                            (((size_t)page * p.Hkv + kvh) * p.page_size + (row & (p.page_size - 1))) * D + key]);
+                        if (fabsf(v) < INFINITY) continue;
+                        const int node = (r0 + c) / p.group - node0, hd = (r0 + c) % p.group;
+                        __nv_bfloat16* x = orow + (size_t)(node * p.Hq + hd) * D;
+                        if (whole)
+                            *x = __float2bfloat16_rn(__bfloat162float(*x) + v);
+                        else
+                            part[c * (D + 4) + key] += v;
                     }
                 }
             }

@@ -231,6 +231,13 @@ struct PiecePlan {
     SeqPlan first;  // plan of request b
 };
 
+// x / y; 64-bit division only where it is needed.
+__device__ __forceinline__ long long quotient(long long x, long long y)
+{
+    if (x <= 0xffffffffll && y <= 0xffffffffll) return (long long)((unsigned)x / (unsigned)y);
+    return x / y;
+}
+
 template <int KT, int RT, int NTHR>
 __device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out, long long* scratch /* [NTHR/32] */)
 {
@@ -238,9 +245,11 @@ __device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out,
     const int each = (p.B + NTHR - 1) / NTHR;
     const int b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
     long long mine = 0;
+    SeqPlan own;  // of request b0, for most threads their only one
     for (int b = b0; b < b1; ++b) {
         const SeqPlan s = seq_plan<KT, RT>(p, b, blockIdx.x == 0);
         mine += (long long)s.items * s.row_tiles * p.Hkv;
+        if (b == b0) own = s;
     }
     long long incl = mine;
 #pragma unroll
@@ -257,7 +266,7 @@ __device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out,
         total += x;
     }
     long long at = before + incl - mine;  // first item of this thread's requests
-    long long per = (total + gridDim.x - 1) / gridDim.x;
+    long long per = quotient(total + gridDim.x - 1, gridDim.x);
     if (per < min_items) per = min_items;
     const long long start = min(total, per * blockIdx.x), end = min(total, start + per);
     if (tid == 0) {
@@ -267,7 +276,7 @@ __device__ void piece_plan(const PagedProblem& p, int min_items, PiecePlan* out,
     }
     if (start < end && at <= start && start < at + mine) {
         for (int b = b0; b < b1; ++b) {
-            const SeqPlan s = seq_plan<KT, RT>(p, b, false);
+            const SeqPlan s = b == b0 ? own : seq_plan<KT, RT>(p, b, false);
             const long long c = (long long)s.items * s.row_tiles * p.Hkv;
             if (at <= start && start < at + c) {
                 out->b = b;
@@ -291,7 +300,7 @@ __device__ __forceinline__ void note_cut(const PagedProblem& p, const SeqPlan& s
 {
     CutUnit* c = reinterpret_cast<CutUnit*>(p.workspace) + blockIdx.x;
     c->rows = rows;
-    c->pieces = (int)((first + s.items - 1) / per - first / per + 1);
+    c->pieces = (int)(quotient(first + s.items - 1, per) - quotient(first, per) + 1);
     c->node0 = s.n0;
     c->head0 = kvh * p.group;
     c->r0 = r0;

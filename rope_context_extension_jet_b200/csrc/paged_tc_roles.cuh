@@ -57,8 +57,7 @@ struct Notes {
     static constexpr int UNIT = BASE;
     static constexpr int U_ANC = 0, U_DEPTH = U_ANC + ROWS * 8, U_LIM = U_DEPTH + kMaxNodes * 4, U_QG = U_LIM + ROWS * 4;
     static constexpr int U_CQ = U_QG + ROWS * 4, U_BIG = U_CQ + ROWS * 4, UBYTES = U_BIG + 16;
-    static constexpr int QS = UNIT + 2 * UBYTES;            // [ROWS] query scales
-    static constexpr int PAR = QS + ROWS * 4;               // [64] parents, [64] node ancestors
+    static constexpr int PAR = UNIT + 2 * UBYTES;           // [64] parents, [64] node ancestors
     static constexpr int KSC = PAR + kMaxNodes * 12;        // [INFO][128] inverse key scales
     static constexpr int TURNS = KSC + INFO * KT * 4;       // [D / 2] phase constants (hi, lo)
     static constexpr int NOTE = TURNS + D / 2 * 8;          // [INFO] mask of the pages present
@@ -270,7 +269,7 @@ __device__ __forceinline__ uint32_t start_cta(const Role<C>& ro, InitExtra init_
 {
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem_base() + C::SLOT);
     const int tid = threadIdx.x;
-    if (tid == 0) {
+    if (tid == C::THREADS - 1) {  // (the first threads go on to the requests' lengths)
         Bars<C> bars;
         bars.init();
         init_extra();
@@ -407,8 +406,8 @@ __device__ __forceinline__ void plan_units(const Role<C>& ro)
     const PiecePlan* plan = reinterpret_cast<const PiecePlan*>(smem_base() + C::PLAN);
     const Bars<C> bars;
     if (ro.lane == 0) {
-        clear_cut(p);
         long long cur = plan->start, base = plan->base;
+        clear_cut(p);
         const long long end = *ro.abort_flag() ? cur : plan->end;
         int b = plan->b, k = 0;
         SeqPlan s = plan->first;
@@ -440,14 +439,14 @@ __device__ __forceinline__ void plan_units(const Role<C>& ro)
                 u.kE0 = s.kE0;
                 u.w0 = s.w0;
                 u.items = s.items;
-                if (u.i0 == 0 && u.i1 < s.items) note_cut(p, s, plan->per, cur, u.kvh, u.r0, u.rows);
-                cur += u.i1 - u.i0;
             }
             if (k >= UNITS && !tc::wait_or_abort(&bars.dfree[k % UNITS], ((k / UNITS) - 1) & 1, ro.abort_flag(), ro.ln.dev_error, ro.ln.wait_cycles, 0x441))
                 break;
             reinterpret_cast<UnitDesc*>(smem_base() + C::DESC)[k % UNITS] = u;
             mbar_arrive(&bars.dfull[k % UNITS]);
             if (u.rows == 0) break;
+            if (u.i0 == 0 && u.i1 < s.items) note_cut(p, s, plan->per, cur, u.kvh, u.r0, u.rows);
+            cur += u.i1 - u.i0;
         }
     }
     __syncwarp();
@@ -521,7 +520,6 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
     };
     int* par = reinterpret_cast<int*>(smem + C::PAR);
     unsigned long long* nanc = reinterpret_cast<unsigned long long*>(par + kMaxNodes);
-    float* qsc = reinterpret_cast<float*>(smem + C::QS);
     int e = 0, nu = 0;
     // A wait that runs out in one warp must not leave the others at a barrier:
     // the warps meet once per unit (and once after the last) and stop together
@@ -545,6 +543,17 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
              (e == 0 || ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x422));
         if ((agreed = named_or(1, C::ROTALL, !ok))) break;
         const int L = ud->L, T = ud->T, n = L + T, rows = ud->rows, r0 = ud->r0, kvh = ud->kvh, n0 = ud->n0;
+        // up to ROTALL / CH rows: a thread holds one chunk of one query for the whole unit,
+        // on its way while the tree is read
+        constexpr bool ONE = C::ROWS * CH <= C::ROTALL;
+        const int own_row = ONE ? t / CH : 0, own_node = ONE ? min((r0 + own_row) / p.group, T - 1) : 0;
+        uint4 own_lo = make_uint4(0u, 0u, 0u, 0u), own_hi = own_lo;
+        if (ONE && own_row < rows) {
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
+                                     ((size_t)(n0 + own_node) * p.Hq + kvh * p.group + (r0 + own_row) % p.group) * D + c * 8;
+            own_lo = *reinterpret_cast<const uint4*>(q);
+            own_hi = *reinterpret_cast<const uint4*>(q + H);
+        }
         if (t < T) {
             int x = t - 1;
             if (p.parents) {
@@ -568,64 +577,71 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             depth[t] = __popcll(m) - 1;
         }
         named_sync(1, C::ROTALL);
-        // The unit's queries turned for the phase of group size g, as fp16.  A task is a
-        // chunk of `span` heads of one node, which share their angles: one head where that
-        // gives every thread at most one task.  The first time also the rows' notes: each
-        // query is multiplied by a power of two that brings its largest element into
-        // [2^13, 2^14), its logits by the inverse.
+        // The unit's queries turned for the phase of group size g, as fp16.  The first time
+        // also the rows' notes: each query is multiplied by a power of two that brings its
+        // largest element into [2^13, 2^14), its logits by the inverse.
+        //
+        // One chunk of one query, by CH lanes that share the row:
+        auto query = [&](bool live, int node, int row, uint4 lo, uint4 hi, const Angles& by, bool setup) {
+            uint32_t mx = mag16(absmax8(lo, hi));
+#pragma unroll
+            for (int o = 1; o < CH; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int ex = tc::range_exp(mx);
+            const float sc = tc::pow2i(ex);
+            if (setup) {
+                float l1 = sum8(lo) + sum8(hi);
+#pragma unroll
+                for (int o = 1; o < CH; o <<= 1) l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+                if (c == 0 && live) {
+                    const int pos = L + depth[node];
+                    lim0[row] = pos - ud->w0;
+                    qG[row] = pos / p.w_pre + 1;
+                    canc[row] = nanc[node];
+                    // a normal number: -inf times it stays -inf
+                    cq[row] = fminf(fmaxf(tc::pow2i(-ex) * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);
+                    // keys rounded to fp16 as they are err by up to 2^-25 where fp16 is
+                    // subnormal; with an L1 norm this large that could reach 2^-11 of a logit
+                    if (!(l1 * p.scale_log2 * 1.4142136f <= 16384.f)) *big = 1;
+                }
+            }
+            if (live) {
+                scale8(lo, sc);
+                scale8(hi, sc);
+                turn(lo, hi, by);
+                *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c)) = lo;
+                *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c + CH)) = hi;
+            }
+        };
+        auto load_query = [&](int node, int h, uint4& lo, uint4& hi) {
+            const __nv_bfloat16* q =
+                static_cast<const __nv_bfloat16*>(p.q) + ((size_t)(n0 + node) * p.Hq + kvh * p.group + h) * D + c * 8;
+            lo = *reinterpret_cast<const uint4*>(q);
+            hi = *reinterpret_cast<const uint4*>(q + H);
+        };
+        // More rows than that: a task is a chunk of `span` heads of one node, which share
+        // their angles.
         const int node0 = r0 / p.group, nodes = (r0 + rows - 1) / p.group - node0 + 1;
-        const int span = rows * CH <= C::ROTALL ? 1 : min(p.group, (rows * CH + C::ROTALL - 1) / C::ROTALL);
+        const int span = min(p.group, (rows * CH + C::ROTALL - 1) / C::ROTALL);
         const int spans = (p.group + span - 1) / span;
         auto queries = [&](int g, bool setup) {
-            const int tasks = nodes * spans * CH, end = (tasks + 31) / 32 * 32;  // whole warps
-#pragma unroll 1
-            for (int x = t; x < end; x += C::ROTALL) {  // CH divides the thread count: chunk x % CH = c
-                const int y = x / CH, node = min(node0 + y / spans, T - 1), h0 = (y % spans) * span;
-                const int pos = L + depth[node];
+            if (ONE) {
                 Angles by;
-                angles((uint32_t)pos / (uint32_t)max(g, 1), by);
+                angles((uint32_t)(L + depth[own_node]) / (uint32_t)max(g, 1), by);
+                query(own_row < rows, own_node, own_row, own_lo, own_hi, by, setup);
+            } else {
+                const int tasks = nodes * spans * CH, end = (tasks + 31) / 32 * 32;  // whole warps
 #pragma unroll 1
-                for (int h = h0; h < h0 + span; ++h) {
-                    const int row = node * p.group + h - r0;
-                    const bool live = x < tasks && h < p.group && row >= 0 && row < rows;
-                    uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                    if (live) {
-                        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                                                 ((size_t)(n0 + node) * p.Hq + kvh * p.group + h) * D + c * 8;
-                        lo = *reinterpret_cast<const uint4*>(q);
-                        hi = *reinterpret_cast<const uint4*>(q + H);
-                    }
-                    float sc;
-                    if (setup) {
-                        uint32_t mx = mag16(absmax8(lo, hi));
-                        float l1 = sum8(lo) + sum8(hi);
-#pragma unroll
-                        for (int o = 1; o < CH; o <<= 1) {
-                            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-                        }
-                        const int ex = tc::range_exp(mx);
-                        sc = tc::pow2i(ex);
-                        if (c == 0 && live) {
-                            lim0[row] = pos - ud->w0;
-                            qG[row] = pos / p.w_pre + 1;
-                            canc[row] = nanc[node];
-                            // a normal number: -inf times it stays -inf
-                            cq[row] = fminf(fmaxf(tc::pow2i(-ex) * p.scale_log2, 1.17549435e-38f), 3.40282347e38f);
-                            qsc[row] = sc;
-                            // keys rounded to fp16 as they are err by up to 2^-25 where fp16 is
-                            // subnormal; with an L1 norm this large that could reach 2^-11 of a logit
-                            if (!(l1 * p.scale_log2 * 1.4142136f <= 16384.f)) *big = 1;
-                        }
-                    } else {
-                        sc = live ? qsc[row] : 1.f;
-                    }
-                    if (live) {
-                        scale8(lo, sc);
-                        scale8(hi, sc);
-                        turn(lo, hi, by);
-                        *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c)) = lo;
-                        *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(row, c + CH)) = hi;
+                for (int x = t; x < end; x += C::ROTALL) {  // CH divides the thread count: chunk x % CH = c
+                    const int y = x / CH, node = min(node0 + y / spans, T - 1), h0 = (y % spans) * span;
+                    Angles by;
+                    angles((uint32_t)(L + depth[node]) / (uint32_t)max(g, 1), by);
+#pragma unroll 1
+                    for (int h = h0; h < h0 + span; ++h) {
+                        const int row = node * p.group + h - r0;
+                        const bool live = x < tasks && h < p.group && row >= 0 && row < rows;
+                        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                        if (live) load_query(node, h, lo, hi);
+                        query(live, node, row, lo, hi, by, setup);
                     }
                 }
             }
