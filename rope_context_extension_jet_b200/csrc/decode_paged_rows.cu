@@ -5,11 +5,13 @@
 //
 //   S [128 rows x 128 keys] = Q_rot [128 x d] K_rot^T      (fp16 operands)
 //   O [128 rows x d]       += P [128 x 128] V              (bf16 operands, P in TMEM)
-// A softmax thread owns one row (one TMEM lane), so the running reference, the sum
-// and the rescale factor are its own and no element needs a per-column factor; from
-// about 32 rows on that beats the form of decode_paged_tc.cu, whose cost per key
-// grows with the rows.  Two softmax warpgroups ("streams") overlap: one computes
-// while the tensor cores work for the other.
+// A softmax thread owns half of a row (64 keys of one TMEM lane), so the running
+// reference, the sum and the rescale factor are its own and no element needs a
+// per-column factor; from about 32 rows on that beats the form of decode_paged_tc.cu,
+// whose cost per key grows with the rows.  Two "streams" (S, O) overlap: the softmax
+// warps take them in turn, all eight on one, while the tensor cores work for the
+// other.  (With one warpgroup per stream a thread held the whole row and had to read
+// half of it from tensor memory twice: 64-node trees at 8 x 32K 404 us instead of 372.)
 //   ROWS = 256: stream s holds rows [128 s, 128 s + 128); both use every key tile,
 //     which is loaded and rotated once for all 256.
 //   ROWS = 128: both hold the same rows and take the tiles in turn; each keeps its
@@ -43,9 +45,10 @@ struct RowTiles {
 };
 template <int D, int NROWS>
 struct RowCfg : RowTiles<D, NROWS>,
-                Notes<D, NROWS, RowTiles<D, NROWS>::NSK, RowTiles<D, NROWS>::NSV, RowTiles<D, NROWS>::BASE, 8, 20> {
-    static constexpr int XCH = RowCfg::NOTES_END;  // [2][128] (reference, sum) of the streams
-    static constexpr int TOTAL = XCH + 2 * 128 * 8 + 1024;
+                Notes<D, NROWS, RowTiles<D, NROWS>::NSK, RowTiles<D, NROWS>::NSV, RowTiles<D, NROWS>::BASE, 6, 20> {
+    static constexpr int XCH = RowCfg::NOTES_END;  // [2][128] sums of both streams over a half's keys
+    static constexpr int TOP = XCH + 2 * 128 * 8;  // [2][128] largest logit of a half's keys
+    static constexpr int TOTAL = TOP + 2 * 128 * 4 + 1024;
     static_assert(TOTAL <= 232448, "shared memory");
     // Registers per thread after setmaxnreg: producers / issuer / planner, the two
     // rotation and the two softmax warpgroups.  640 threads launch with 96 each, and an
@@ -65,13 +68,12 @@ __global__ void __launch_bounds__(640, 1)
     unsigned char* const smem = smem_base();
     const Role<C> ro(p, ln);
     const Bars<C> bars;
-    uint64_t *sfull = bars.extra, *pfull = sfull + 2, *pvdone = pfull + 4;  // per stream; pfull per half of the keys
+    uint64_t *sfull = bars.extra, *pfull = sfull + 2, *pvdone = pfull + 2;  // per stream
     const int warp = ro.warp, lane = ro.lane;
     const uint32_t tmem = start_cta<C, 512>(ro, [&] {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sfull[s], 1);
-            mbar_init(&pfull[2 * s], 4);
-            mbar_init(&pfull[2 * s + 1], 4);
+            mbar_init(&pfull[s], C::SOFT);
             mbar_init(&pvdone[s], 1);
         }
     });
@@ -105,13 +107,12 @@ __global__ void __launch_bounds__(640, 1)
                     if (!ro.wait(&bars.vfix[st], (nfix >> st) & 1, 0x513)) return false;
                     nfix ^= 1u << st;
                 }
+                if (!ro.wait(&pfull[s], done[s] & 1, 0x511)) return false;
+                tc_fence_after();
                 const uint64_t vd = sdesc_sw128(sb + C::V0 + st * C::TILE, C::ATOM_K, 1024);
 #pragma unroll
-                for (int half = 1; half >= 0; --half) {  // in the order the softmax publishes them
-                    if (!ro.wait(&pfull[2 * s + half], done[s] & 1, 0x511)) return false;
-                    tc_fence_after();
-                    umma_pv_k64(tm + 256 + s * 128, tm + s * 128 + 64 * half, vd + 512 * half, IPV, pfirst[s] && half == 1 ? 0u : 1u);
-                }
+                for (int half = 0; half < 2; ++half)
+                    umma_pv_k64(tm + 256 + s * 128, tm + s * 128 + 64 * half, vd + 512 * half, IPV, pfirst[s] && half == 0 ? 0u : 1u);
                 umma_commit_elect(&pvdone[s]);
                 if (!PAIR || s == 1) umma_commit_elect(&bars.vempty[st]);
                 ++done[s];
@@ -166,16 +167,18 @@ __global__ void __launch_bounds__(640, 1)
         regs_inc<C::R_SOFT>();
         // ------------------------------------------------------ softmax
         constexpr int bid = 2;  // named barrier of both warpgroups
-        const int s = (warp - 12) >> 2, lrow = (warp & 3) * 32 + lane, row = (PAIR ? s * 128 : 0) + lrow;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t s_col = lanes + s * 128, o_col = lanes + 256 + s * 128;
+        const int h = (warp - 12) >> 2, quad = warp & 3, lrow = quad * 32 + lane;  // half of the keys; TMEM lane
+        const int pid = 3 + quad;  // named barrier of the two warps that share rows
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         const float* ksc = reinterpret_cast<const float*>(smem + C::KSC);
         float2* xch = reinterpret_cast<float2*>(smem + C::XCH);
+        float* tops = reinterpret_cast<float*>(smem + C::TOP);
         const int gshift = min(p.page_shift, 7);
         const unsigned all_pages = ro.all_pages();
-        int e = 0, nu = 0, done = 0;  // items, units, tasks of this stream
-        // a wait that ran out is carried to the next barrier of the two warpgroups,
-        // where their eight warps stop together
+        int e = 0, nu = 0;
+        int done = 0, done2 = 0;  // tasks of the stream at hand, of the other
+        // a wait that ran out is carried to the next barrier, where the warps that meet
+        // there stop together
         bool ok = true;
         for (;; ++nu) {
             ok = ro.unit_wait(nu, 0x536);
@@ -186,20 +189,30 @@ __global__ void __launch_bounds__(640, 1)
             }
             const unsigned char* un = smem + C::UNIT + (nu & 1) * C::UBYTES;
             const int* depth = reinterpret_cast<const int*>(un + C::U_DEPTH);
+            const float* cqs = reinterpret_cast<const float*>(un + C::U_CQ) + lrow;
+            const unsigned long long* ancs = reinterpret_cast<const unsigned long long*>(un + C::U_ANC) + lrow;
             ok = ok && ro.wait(&bars.uready[nu & 1], (nu >> 1) & 1, 0x531);
-            const int lim = reinterpret_cast<const int*>(un + C::U_LIM)[row], G = reinterpret_cast<const int*>(un + C::U_QG)[row];
-            const float cq = reinterpret_cast<const float*>(un + C::U_CQ)[row];
-            const unsigned long long anc = reinterpret_cast<const unsigned long long*>(un + C::U_ANC)[row];
-            float ref = kNoRef, l = 0.f;
-            unsigned long long nodes = 0;  // drafted nodes this row attends in the current phase
-            int gcur = -1, li = 0, mine = 0;
+            // state of the row of the stream at hand and of the other's; they swap after every task
+            float ref = kNoRef, l = 0.f, ref2 = kNoRef, l2 = 0.f;
+            float cq = cqs[0], cq2 = cqs[PAIR ? 128 : 0];
+            int tasks = 0;
+            auto swap_streams = [&] {
+                float f = ref; ref = ref2; ref2 = f;
+                f = l; l = l2; l2 = f;
+                f = cq; cq = cq2; cq2 = f;
+                const int d = done; done = done2; done2 = d;
+            };
             const int L = ud->L, T = ud->T, near = L + T - 1 - ud->w0;
             const int far = ud->ng > 1 ? -1 : (int)max(-1ll, (long long)L - ud->w0 - (KT - 1));
-            if (ok) {
-                for (UnitItems it(ud); it.left > 0; it.next(), ++e, ++li) {
-                    if (!PAIR && (li & 1) != s) continue;
-                    const int g = it.g, j0 = it.tile * KT;
-                    if (!ro.wait(&sfull[s], done & 1, 0x532)) { ok = false; break; }
+            bool alive = true;  // of the two warps that share rows
+            for (UnitItems it(ud); alive && it.left > 0; it.next(), ++e) {
+                const int g = it.g, j0 = it.tile * KT;
+                // both streams take the tile, or they take tiles in turn
+#pragma unroll 1
+                for (int task = 0; task < (PAIR ? 2 : 1); ++task) {
+                    const int s = tasks & 1;
+                    const uint32_t s_col = lanes + s * 128 + h * 64;
+                    ok = ok && ro.wait(&sfull[s], done & 1, 0x532);
                     tc_fence_after();
                     const unsigned have = ro.note()[e % INFO];
                     const volatile unsigned* flags = reinterpret_cast<const volatile unsigned*>(smem + C::SCALED) + (e % INFO) * 8;
@@ -208,225 +221,221 @@ __global__ void __launch_bounds__(640, 1)
                     for (int w = 0; w < C::ROT / 32; ++w) any_scaled |= flags[w];
                     const bool drafted = j0 + KT > L || have != all_pages;
                     const bool masked = drafted || (g == 0 ? j0 <= near : j0 > far);
-                    uint32_t bits[4];  // masked tiles: the keys of the tile that belong to this row and item
+                    float x[KT / 2];
+                    {
+                        uint32_t t0[32], t1[32];
+                        tmem_ld32(s_col, t0);
+                        tmem_ld32(s_col + 32, t1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) {
+                            x[u] = __uint_as_float(t0[u]);
+                            x[32 + u] = __uint_as_float(t1[u]);
+                        }
+                    }
+                    // key rows that were scaled by a power of two (paged_tc_roles.cuh) scaled back
+                    if (any_scaled) {
+                        asm volatile("" ::: "memory");
+                        const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT + h * 64);
+#pragma unroll
+                        for (int u = 0; u < KT / 2; u += 4) {
+                            const float4 f = k4[u / 4];
+                            x[u] *= f.x;
+                            x[u + 1] *= f.y;
+                            x[u + 2] *= f.z;
+                            x[u + 3] *= f.w;
+                        }
+                    }
+                    // what does not belong to this row and item at -inf
                     if (masked) {
                         asm volatile("" ::: "memory");  // a branch, not predication: most tiles skip this
-                        if (g != gcur) {
-                            gcur = g;
-                            nodes = 0;
+                        const int row = (PAIR ? s * 128 : 0) + lrow, k0 = j0 + h * 64;  // first key of the half
+                        const int lim = reinterpret_cast<const int*>(un + C::U_LIM)[row];
+                        const int G = reinterpret_cast<const int*>(un + C::U_QG)[row];
+                        // committed keys: those past the border (exact phase) or up to it
+                        // (remote phase of this row's group size), before row L
+                        const int cut = lim < k0 ? 0 : lim - k0 + 1;  // keys [0, cut) of the half are remote
+                        const int c0 = L - k0;                        // keys [0, c0) are committed
+                        auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+                        unsigned long long keep = below(cut);
+                        keep = g == 0 ? ~keep : (G == g ? keep : 0ull);
+                        keep &= below(c0);
+                        if (drafted) {
+                            const unsigned long long anc = ancs[PAIR ? s * 128 : 0];
+                            unsigned long long nodes = 0;  // drafted nodes this row attends in this phase
 #pragma unroll 1
                             for (int v = 0; v < T; ++v) {
                                 const bool local = L + depth[v] > lim;
-                                const bool keep = g == 0 ? local : (!local && G == g);
-                                nodes |= (unsigned long long)(keep && ((anc >> v) & 1)) << v;
+                                const bool in = g == 0 ? local : (!local && G == g);
+                                nodes |= (unsigned long long)(in && ((anc >> v) & 1)) << v;
+                            }
+                            // node v is key c0 + v
+                            if (c0 > -64 && c0 < 64) keep |= c0 >= 0 ? nodes << c0 : nodes >> -c0;
+                            if (have != all_pages) {
+                                unsigned long long there = 0;
+#pragma unroll 1
+                                for (int u = 0; u < 64; ++u) there |= (unsigned long long)((have >> ((h * 64 + u) >> gshift)) & 1u) << u;
+                                keep &= there;
                             }
                         }
-                        // committed keys: those past the border (exact phase) or up to it
-                        // (remote phase of this row's group size), before row L
-                        const int cut = lim < j0 ? 0 : lim - j0 + 1;  // keys [0, cut) of the tile are remote
-                        const int c0 = L - j0;                        // keys [0, c0) are committed
+                        const uint32_t b0 = (uint32_t)keep, b1 = (uint32_t)(keep >> 32);
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            auto below = [&](int n) {  // bits of this word's keys that lie in [0, n) of the tile
-                                const int m = n - 32 * w;
-                                return m <= 0 ? 0u : m >= 32 ? 0xffffffffu : (1u << m) - 1;
-                            };
-                            uint32_t o = below(cut);
-                            o = g == 0 ? ~o : (G == g ? o : 0u);
-                            o &= below(c0);
-                            // node v is key c0 + v
-                            const int sh = 32 * w - c0;
-                            if (sh >= 0)
-                                o |= sh < 64 ? (uint32_t)(nodes >> sh) : 0u;
-                            else if (sh > -32)
-                                o |= (uint32_t)nodes << -sh;
-                            if (have != all_pages) {
-                                uint32_t there = 0;
-#pragma unroll 1
-                                for (int u = 0; u < 32; ++u) there |= ((have >> ((32 * w + u) >> gshift)) & 1u) << u;
-                                o &= there;
-                            }
-                            bits[w] = o;
+                        for (int u = 0; u < 32; ++u) {
+                            x[u] = (b0 >> u) & 1 ? x[u] : -INFINITY;
+                            x[32 + u] = (b1 >> u) & 1 ? x[32 + u] : -INFINITY;
                         }
                         __syncwarp();
                     }
-                    // 64 keys of the row; key rows that were scaled by a power of two
-                    // (paged_tc_roles.cuh) scaled back, what does not belong at -inf
-                    float x[KT / 2];
-                    auto load = [&](int half) {
-                        {
-                            uint32_t t0[32], t1[32];
-                            tmem_ld32(s_col + half * 64, t0);
-                            tmem_ld32(s_col + half * 64 + 32, t1);
-                            tmem_wait_ld();
+                    float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) {
-                                x[u] = __uint_as_float(t0[u]);
-                                x[32 + u] = __uint_as_float(t1[u]);
-                            }
+                    for (int u = 4; u < KT / 2; u += 8) {
+                        m4[0] = fmax3(m4[0], x[u], x[u + 1]);
+                        m4[1] = fmax3(m4[1], x[u + 2], x[u + 3]);
+                        if (u + 4 < KT / 2) {
+                            m4[2] = fmax3(m4[2], x[u + 4], x[u + 5]);
+                            m4[3] = fmax3(m4[3], x[u + 6], x[u + 7]);
                         }
-                        if (any_scaled) {
-                            asm volatile("" ::: "memory");
-                            const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT + half * 64);
-#pragma unroll
-                            for (int u = 0; u < KT / 2; u += 4) {
-                                const float4 f = k4[u / 4];
-                                x[u] *= f.x;
-                                x[u + 1] *= f.y;
-                                x[u + 2] *= f.z;
-                                x[u + 3] *= f.w;
-                            }
-                        }
-                        if (masked) {
-                            asm volatile("" ::: "memory");
-                            const uint32_t b0 = half ? bits[2] : bits[0], b1 = half ? bits[3] : bits[1];
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) {
-                                x[u] = (b0 >> u) & 1 ? x[u] : -INFINITY;
-                                x[32 + u] = (b1 >> u) & 1 ? x[32 + u] : -INFINITY;
-                            }
-                        }
-                    };
-                    // the row's largest logit over both halves; the second stays in registers
-                    // (half the tile at a time keeps the softmax at 128 registers, which is
-                    // what makes room for two rotation warpgroups)
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        load(half);
-                        float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                        for (int u = 4; u < KT / 2; u += 8) {
-                            m4[0] = fmax3(m4[0], x[u], x[u + 1]);
-                            m4[1] = fmax3(m4[1], x[u + 2], x[u + 3]);
-                            if (u + 4 < KT / 2) {
-                                m4[2] = fmax3(m4[2], x[u + 4], x[u + 5]);
-                                m4[3] = fmax3(m4[3], x[u + 6], x[u + 7]);
-                            }
-                        }
-                        top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                     }
+                    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     // logits in log2 units: x cq, cq > 0 a power of two times the scale
-                    const float mt = top * cq;
-                    float alpha = 1.f;
-                    const bool resc = mt > ref + kExceed;
-                    if (resc) {
-                        alpha = ex2_approx(ref - (mt + kAbove));
-                        ref = mt + kAbove;
-                        l *= alpha;
-                    }
-                    // O is rescaled before any of this tile's P is published
-                    if (mine > 0 && __any_sync(0xffffffffu, resc)) {
-                        if (!ro.wait(&pvdone[s], (done - 1) & 1, 0x533)) { ok = false; break; }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int cc = 0; cc < D; cc += 16) {
-                            uint32_t tt[16];
-                            tmem_ld16(o_col + cc, tt);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int u = 0; u < 16; ++u) tt[u] = __float_as_uint(__uint_as_float(tt[u]) * alpha);
-                            tmem_st16(o_col + cc, tt);
+                    if (named_or(pid, 64, top * cq > ref + kExceed || !ok)) {
+                        // some row's reference moves: both halves of its keys follow
+                        asm volatile("" ::: "memory");
+                        tops[h * 128 + lrow] = top;
+                        if (named_or(pid, 64, !ok)) {
+                            alive = false;
+                            break;
                         }
-                        tmem_wait_st();
+                        const float mt = fmaxf(top, tops[(h ^ 1) * 128 + lrow]) * cq;
+                        const bool resc = mt > ref + kExceed;
+                        float alpha = 1.f;
+                        if (resc) {
+                            alpha = ex2_approx(ref - (mt + kAbove));
+                            ref = mt + kAbove;
+                            l *= alpha;
+                        }
+                        // O (a half of its columns each) follows before any of this tile's P is published
+                        if (tasks > 1 && __any_sync(0xffffffffu, resc)) {
+                            ok = ro.wait(&pvdone[s], (done - 1) & 1, 0x533);
+                            tc_fence_after();
+                            const uint32_t o_col = lanes + 256 + s * 128 + h * (D / 2);
+#pragma unroll 1
+                            for (int cc = 0; cc < D / 2; cc += 16) {
+                                uint32_t tt[16];
+                                tmem_ld16(o_col + cc, tt);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) tt[u] = __float_as_uint(__uint_as_float(tt[u]) * alpha);
+                                tmem_st16(o_col + cc, tt);
+                            }
+                            tmem_wait_st();
+                        }
                     }
                     const float2 sl = make_float2(cq, cq), nm = make_float2(-ref, -ref);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
                     // the stream's last P V finished before this tile's Q K^T (issued later by
                     // the same issuer), so each half of P may go over its half of S
-#pragma unroll 1
-                    for (int half = 1; half >= 0; --half) {
-                        if (half == 0) load(0);
-                        uint32_t pk[KT / 4];
+                    uint32_t pk[KT / 4];
 #pragma unroll
-                        for (int u = 0; u < KT / 2; u += 4) {
-                            const float2 y0 = fma2(make_float2(x[u], x[u + 1]), sl, nm);
-                            const float2 y1 = fma2(make_float2(x[u + 2], x[u + 3]), sl, nm);
-                            const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
-                            const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
-                            acc0 = add2(acc0, p0);
-                            acc1 = add2(acc1, p1);
-                            pk[u >> 1] = pack_bf16x2(p0.x, p0.y);
-                            pk[(u >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
-                        }
-                        tmem_st32(s_col + half * 64, pk);
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&pfull[2 * s + half]);
+                    for (int u = 0; u < KT / 2; u += 4) {
+                        const float2 y0 = fma2(make_float2(x[u], x[u + 1]), sl, nm);
+                        const float2 y1 = fma2(make_float2(x[u + 2], x[u + 3]), sl, nm);
+                        const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
+                        const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+                        acc0 = add2(acc0, p0);
+                        acc1 = add2(acc1, p1);
+                        pk[u >> 1] = pack_bf16x2(p0.x, p0.y);
+                        pk[(u >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
                     }
-                    if (!ok) break;
+                    tmem_st32(s_col, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[s]);
                     l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
                     ++done;
-                    ++mine;
+                    ++tasks;
+                    swap_streams();
                 }
             }
             // ---- the unit's piece is complete
-            if (ok && mine > 0) ok = ro.wait(&pvdone[s], (done - 1) & 1, 0x535);
-            if (!PAIR) xch[s * 128 + lrow] = make_float2(ref, l);
+            if (tasks & 1) swap_streams();  // back to stream 0 first
+            if (ok && tasks > 0) ok = ro.wait(&pvdone[0], (done - 1) & 1, 0x535);
+            if (ok && tasks > 1) ok = ro.wait(&pvdone[1], (done2 - 1) & 1, 0x537);
+            xch[h * 128 + lrow] = make_float2(l, l2);
             tc_fence_before();
             if (named_or(bid, 256, !ok)) break;
             tc_fence_after();
-            const int i0 = ud->i0, r0 = ud->r0, kvh = ud->kvh, rows = ud->rows;
-            const bool whole = i0 == 0 && ud->i1 == ud->items, live = row < rows;
-            float w0 = 1.f, w1 = 0.f;  // weights of this and the other stream's O
+            {
+                const float2 o = xch[(h ^ 1) * 128 + lrow];
+                l += o.x;
+                l2 += o.y;
+            }
+            float w0 = 1.f, w1 = 0.f;  // weights of the streams' O
             if (!PAIR) {
-                const float2 o = xch[(s ^ 1) * 128 + lrow];
-                const float top = fmaxf(ref, o.x);
+                const float top = fmaxf(ref, ref2);
                 w0 = ref == kNoRef ? 0.f : ex2_approx(ref - top);
-                w1 = o.x == kNoRef ? 0.f : ex2_approx(o.x - top);
-                l = w0 * l + w1 * o.y;
+                w1 = ref2 == kNoRef ? 0.f : ex2_approx(ref2 - top);
+                l = w0 * l + w1 * l2;
                 ref = top;
             }
-            const unsigned long long bad = ud->bad & anc;
-            const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
-            float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
-                          (((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NROWS + row) * (D + 4);
-            __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + ((size_t)(ud->n0 + node) * p.Hq + hd) * D;
-            const float inv = 1.f / l;
-            // the streams of one row share its columns
-            const int cb0 = PAIR ? 0 : s * (D / 2), cb1 = PAIR ? D : cb0 + D / 2;
+            const int i0 = ud->i0, r0 = ud->r0, kvh = ud->kvh, rows = ud->rows;
+            const bool whole = i0 == 0 && ud->i1 == ud->items;
+            const unsigned long long all_bad = ud->bad;
 #pragma unroll 1
-            for (int cb = cb0; cb < cb1; cb += 16) {
-                uint32_t a[16], b[16];
-                tmem_ld16(o_col + cb, a);
-                if (!PAIR) tmem_ld16(lanes + 256 + (s ^ 1) * 128 + cb, b);
-                tmem_wait_ld();
-                float v[16];
+            for (int s = 0; s < (PAIR ? 2 : 1); ++s) {
+                const int row = s * 128 + lrow;
+                const bool live = row < rows;
+                const unsigned long long bad = all_bad & ancs[s * 128];
+                const int node = (r0 + row) / p.group, hd = kvh * p.group + (r0 + row) % p.group;
+                float* part = reinterpret_cast<float*>(p.workspace + kPagedHeader) +
+                              (((size_t)blockIdx.x * 2 + (i0 == 0 ? 1 : 0)) * NROWS + row) * (D + 4);
+                __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + ((size_t)(ud->n0 + node) * p.Hq + hd) * D;
+                const float inv = 1.f / l;
+#pragma unroll 1
+                for (int cb = h * (D / 2); cb < (h + 1) * (D / 2); cb += 16) {
+                    uint32_t a[16], b[16];
+                    tmem_ld16(lanes + 256 + s * 128 + cb, a);
+                    if (!PAIR) tmem_ld16(lanes + 256 + 128 + cb, b);
+                    tmem_wait_ld();
+                    float v[16];
 #pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    v[u] = __uint_as_float(a[u]);
-                    if (!PAIR)  // a stream without a key of this row holds no values
-                        v[u] = (w0 != 0.f ? w0 * v[u] : 0.f) + (w1 != 0.f ? w1 * __uint_as_float(b[u]) : 0.f);
-                }
-                if (live && bad) {
-                    // infinities and NaN of drafted rows this node attends
-                    for (unsigned long long rest = bad; rest; rest &= rest - 1) {
-                        const int r = ud->L + __ffsll((long long)rest) - 1;
-                        const int page = p.table[(size_t)ud->b * p.max_pages + (r >> p.page_shift)];
-                        const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.vc) +
-                                                  (((size_t)page * p.Hkv + kvh) * p.page_size + (r & (p.page_size - 1))) * D + cb;
+                    for (int u = 0; u < 16; ++u) {
+                        v[u] = __uint_as_float(a[u]);
+                        if (!PAIR)  // a stream without a key of this row holds no values
+                            v[u] = (w0 != 0.f ? w0 * v[u] : 0.f) + (w1 != 0.f ? w1 * __uint_as_float(b[u]) : 0.f);
+                    }
+                    if (live && bad) {
+                        // infinities and NaN of drafted rows this node attends
+                        for (unsigned long long rest = bad; rest; rest &= rest - 1) {
+                            const int r = ud->L + __ffsll((long long)rest) - 1;
+                            const int page = p.table[(size_t)ud->b * p.max_pages + (r >> p.page_shift)];
+                            const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.vc) +
+                                                      (((size_t)page * p.Hkv + kvh) * p.page_size + (r & (p.page_size - 1))) * D + cb;
 #pragma unroll
-                        for (int u = 0; u < 16; ++u) {
-                            const float f = __bfloat162float(vr[u]);
-                            if (!(fabsf(f) < INFINITY)) v[u] += f;
+                            for (int u = 0; u < 16; ++u) {
+                                const float f = __bfloat162float(vr[u]);
+                                if (!(fabsf(f) < INFINITY)) v[u] += f;
+                            }
                         }
                     }
-                }
-                if (live && whole) {
+                    if (live && whole) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        *reinterpret_cast<uint4*>(orow + cb + q * 8) =
-                            make_uint4(pack_bf16x2(v[8 * q] * inv, v[8 * q + 1] * inv), pack_bf16x2(v[8 * q + 2] * inv, v[8 * q + 3] * inv),
-                                       pack_bf16x2(v[8 * q + 4] * inv, v[8 * q + 5] * inv), pack_bf16x2(v[8 * q + 6] * inv, v[8 * q + 7] * inv));
-                } else if (live) {
+                        for (int q = 0; q < 2; ++q)
+                            *reinterpret_cast<uint4*>(orow + cb + q * 8) =
+                                make_uint4(pack_bf16x2(v[8 * q] * inv, v[8 * q + 1] * inv), pack_bf16x2(v[8 * q + 2] * inv, v[8 * q + 3] * inv),
+                                           pack_bf16x2(v[8 * q + 4] * inv, v[8 * q + 5] * inv), pack_bf16x2(v[8 * q + 6] * inv, v[8 * q + 7] * inv));
+                    } else if (live) {
 #pragma unroll
-                    for (int u = 0; u < 16; u += 4)
-                        *reinterpret_cast<float4*>(part + cb + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+                        for (int u = 0; u < 16; u += 4)
+                            *reinterpret_cast<float4*>(part + cb + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+                    }
                 }
+                if (live && !whole && h == 0)
+                    *reinterpret_cast<float2*>(part + D) = make_float2(ref == kNoRef ? -INFINITY : ref, l);
+                ref = ref2;
+                l = l2;
             }
-            if (live && !whole && (PAIR || s == 0))
-                *reinterpret_cast<float2*>(part + D) = make_float2(ref == kNoRef ? -INFINITY : ref, l);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.ufree[nu & 1]);
