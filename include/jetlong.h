@@ -373,9 +373,11 @@ int jetlong_selftest_wait_timeout(void* stream);
  *       the first key tile of every work unit is never released to the MMA
  *       issuer.
  *   JETLONG_INJECT_DECODE_COPY: bf16 decode: the first K/V stage of every
- *       key split is never loaded.
+ *       key split is never loaded.  Paged decode (both dtypes): the first key
+ *       tile of every CTA's share of the keys is never loaded.
  * The hook is consumed by the next prefill or decode call of this thread that
- * passes argument validation (whatever its dtype; the fp32 kernels ignore it);
+ * passes argument validation (whatever its dtype; the fp32 prefill and the fp32
+ * decode over a contiguous cache ignore it);
  * JETLONG_INJECT_NONE disarms it.  wait_cycles in [1e4, 4e9] (ignored for
  * JETLONG_INJECT_NONE).  Returns JETLONG_OK or JETLONG_ERR_INVALID_ARG. */
 #define JETLONG_INJECT_NONE 0

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
                     const unsigned have = __ballot_sync(0xffffffffu, lane < nbox && page >= 0);
                     const int st = e % C::NS;
                     if (e >= C::NS &&
-                        !tc::warp_wait(&empty[st], ((e / C::NS) - 1) & 1, abort_flag, p.dev_error, wait_cycles, 0x601)) {
+                        !tc::warp_wait(&empty[st], ((e / C::NS) - 1) & 1, abort_flag, p.dev_error, wait_cycles, 0x701)) {
                         ok = false;
                         break;
                     }
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(NTHR, 1) decode_paged_fp32_kernel(const __grid
             // this key group's tiles of the phase
             for (int x = (kg - e % C::WK + C::WK) % C::WK; x < cnt; x += C::WK) {
                 const int ee = e + x, st = ee % C::NS, j0 = (tile0 + x) * KT;
-                if (!tc::warp_wait(&full[ee % C::NB], (ee / C::NB) & 1, abort_flag, p.dev_error, wait_cycles, 0x611)) {
+                if (!tc::warp_wait(&full[ee % C::NB], (ee / C::NB) & 1, abort_flag, p.dev_error, wait_cycles, 0x711)) {
                     ok = false;
                     break;
                 }

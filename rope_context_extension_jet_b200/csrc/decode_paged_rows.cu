@@ -18,7 +18,7 @@
 //     own reference, sum and O, joined where the unit ends.
 //
 // Warp roles: 0 / 3 producers, 1 MMA issuer, 2 tensor memory and planner, 4-11
-// rotation, 12-15 / 16-19 softmax of stream 0 / 1.
+// rotation, 12-15 / 16-19 softmax of the first / second 64 keys of a tile.
 // TMEM (512 columns): S_0, S_1 (128 each; the halves of P_s over columns 0-31 and
 // 64-95 of S_s, each over the half of S_s it was made from), O_0, O_1.
 #include <algorithm>

@@ -116,11 +116,11 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
         bool ok = true;
         // O^T += V^T P^T of item x
         auto pv = [&](int x, bool first, bool fix) {
-            if (!ro.wait(&pfull[x & 1], (x >> 1) & 1, 0x411)) return false;
+            if (!ro.wait(&pfull[x & 1], (x >> 1) & 1, 0x611)) return false;
             const int st = x % NSV;
-            if (!ro.wait(&bars.vfull[st], (x / NSV) & 1, 0x412)) return false;
+            if (!ro.wait(&bars.vfull[st], (x / NSV) & 1, 0x612)) return false;
             if (fix) {
-                if (!ro.wait(&bars.vfix[st], (nfix >> st) & 1, 0x413)) return false;
+                if (!ro.wait(&bars.vfix[st], (nfix >> st) & 1, 0x613)) return false;
                 nfix ^= 1u << st;
             }
             tc_fence_after();
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
         int phases = 0;
         const unsigned all_pages = ro.all_pages();
         for (int k = 0; ok; ++k) {
-            if (!ro.unit_wait(k, 0x416)) { ok = false; break; }
+            if (!ro.unit_wait(k, 0x616)) { ok = false; break; }
             UnitPtr un = ro.unit(k);
             if (un->rows == 0) break;
             const int L = un->L;
@@ -146,10 +146,10 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                 const int st = e % NSK;
                 if (it.g != gcur) {
                     gcur = it.g;
-                    if (!ro.wait(bars.qready, phases & 1, 0x415)) { ok = false; break; }
+                    if (!ro.wait(bars.qready, phases & 1, 0x615)) { ok = false; break; }
                     ++phases;
                 }
-                if (!ro.wait(&bars.kready[st], (e / NSK) & 1, 0x414)) { ok = false; break; }
+                if (!ro.wait(&bars.kready[st], (e / NSK) & 1, 0x614)) { ok = false; break; }
                 const bool fix = (it.tile + 1) * KT > L || ro.note()[e % INFO] != all_pages;
                 tc_fence_after();
                 const uint64_t a = sdesc_sw128(sb + C::K0 + st * C::TILE, 16, 1024);
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
         const int gshift = min(p.page_shift, 7);
         const unsigned all_pages = ro.all_pages();
         for (; !stop; ++nu) {
-            ok = ro.unit_wait(nu, 0x436);
+            ok = ro.unit_wait(nu, 0x636);
             UnitPtr ud = ro.unit(nu);
             if (ok && ud->rows == 0) {
                 named_or(bid, 128, false);  // meets a warp that gave up waiting for the unit
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             const int* qG = reinterpret_cast<const int*>(un + C::U_QG);
             const float* cq = reinterpret_cast<const float*>(un + C::U_CQ);
             const unsigned long long* canc = reinterpret_cast<const unsigned long long*>(un + C::U_ANC);
-            ok = ok && ro.wait(&bars.uready[nu & 1], (nu >> 1) & 1, 0x431);
+            ok = ok && ro.wait(&bars.uready[nu & 1], (nu >> 1) & 1, 0x631);
 #pragma unroll
             for (int c = 0; c < NCOL; ++c) l[c] = 0.f;
             if (key < NCOL) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             bool first = true;
             for (UnitItems it(ud); it.left > 0; it.next(), ++e) {
                 const int g = it.g, j0 = it.tile * KT;
-                ok = ok && ro.wait(&sfull[e & 1], (e >> 1) & 1, 0x432);
+                ok = ok && ro.wait(&sfull[e & 1], (e >> 1) & 1, 0x632);
                 tc_fence_after();
                 const unsigned have = ro.note()[e % INFO];
                 // which pairs of the tile this item leaves out: some of a drafted or
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                     for (int c = 0; c < NCOL; ++c)
                         if ((c & ~15) < cols) l[c] *= alpha[c];
                     if (!first) {
-                        ok = ro.wait(&pvdone[(e - 1) & 1], ((e - 1) >> 1) & 1, 0x433);
+                        ok = ro.wait(&pvdone[(e - 1) & 1], ((e - 1) >> 1) & 1, 0x633);
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < NCOL; c += 16) {
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             }
             if (stop) break;
             // ---- the unit's piece is complete
-            ok = ok && ro.wait(&pvdone[(e - 1) & 1], ((e - 1) >> 1) & 1, 0x435);
+            ok = ok && ro.wait(&pvdone[(e - 1) & 1], ((e - 1) >> 1) & 1, 0x635);
             tc_fence_after();
 #pragma unroll
             for (int cb = 0; cb < NCOL; cb += 16) {

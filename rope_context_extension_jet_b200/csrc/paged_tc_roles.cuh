@@ -312,7 +312,7 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
     int e = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-        if (!ro.unit_wait(k, isK ? 0x403 : 0x404)) break;
+        if (!ro.unit_wait(k, isK ? 0x603 : 0x604)) break;
         UnitPtr un = ro.unit(k);
         if (un->rows == 0) break;
         const int* table = p.table + (size_t)un->b * p.max_pages;
@@ -330,7 +330,7 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
                 }
             }
             const int st = e % NS;
-            if (e >= NS && !ro.wait(&empty[st], ((e / NS) - 1) & 1, isK ? 0x401 : 0x402)) { ok = false; break; }
+            if (e >= NS && !ro.wait(&empty[st], ((e / NS) - 1) & 1, isK ? 0x601 : 0x602)) { ok = false; break; }
             const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
             const bool skip = isK && e == 0 && ln.inject == kInjectDecodeCopy;  // test hook: the first key tile is never loaded
             if (lane == 0) {
@@ -354,7 +354,7 @@ __device__ __forceinline__ void produce(const Role<C>& ro, const CUtensorMap* tm
                 // there, and a weight of 0 does not silence NaN.  A drafted row's own
                 // infinities and NaN are cleared as well (nodes beside it must not see
                 // them) and noted for the nodes that do attend it.
-                if (!ro.wait(&full[e % NF], (e / NF) & 1, 0x405)) {
+                if (!ro.wait(&full[e % NF], (e / NF) & 1, 0x605)) {
                     ++e;  // its copy is in flight
                     ok = false;
                     break;
@@ -440,7 +440,7 @@ __device__ __forceinline__ void plan_units(const Role<C>& ro)
                 u.w0 = s.w0;
                 u.items = s.items;
             }
-            if (k >= UNITS && !tc::wait_or_abort(&bars.dfree[k % UNITS], ((k / UNITS) - 1) & 1, ro.abort_flag(), ro.ln.dev_error, ro.ln.wait_cycles, 0x441))
+            if (k >= UNITS && !tc::wait_or_abort(&bars.dfree[k % UNITS], ((k / UNITS) - 1) & 1, ro.abort_flag(), ro.ln.dev_error, ro.ln.wait_cycles, 0x641))
                 break;
             reinterpret_cast<UnitDesc*>(smem_base() + C::DESC)[k % UNITS] = u;
             mbar_arrive(&bars.dfull[k % UNITS]);
@@ -526,7 +526,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
     // if any of them gave up.
     bool ok = true, agreed = false;
     for (; ok; ++nu) {
-        ok = ro.unit_wait(nu, 0x426);
+        ok = ro.unit_wait(nu, 0x626);
         UnitPtr ud = ro.unit(nu);
         if (ok && ud->rows == 0) break;
         unsigned char* un = smem + C::UNIT + (nu & 1) * C::UBYTES;
@@ -539,8 +539,8 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
         // the softmax is done with unit nu - 2, the tensor cores with the queries of
         // unit nu - 1 (known to the warps that rotated item e - 1, and through the
         // barrier to the others)
-        ok = ok && (nu < 2 || ro.wait(&bars.ufree[nu & 1], ((nu >> 1) - 1) & 1, 0x421)) &&
-             (e == 0 || ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x422));
+        ok = ok && (nu < 2 || ro.wait(&bars.ufree[nu & 1], ((nu >> 1) - 1) & 1, 0x621)) &&
+             (e == 0 || ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x622));
         if ((agreed = named_or(1, C::ROTALL, !ok))) break;
         const int L = ud->L, T = ud->T, n = L + T, rows = ud->rows, r0 = ud->r0, kvh = ud->kvh, n0 = ud->n0;
         // up to ROTALL / CH rows: a thread holds one chunk of one query for the whole unit,
@@ -677,7 +677,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                 // the next phase; the tensor cores are done with the queries of the last
                 // (only the warps that rotated item e - 1 know that the wait is for its phase:
                 // the others follow through the barrier)
-                ok = ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x423);
+                ok = ro.wait(&bars.kempty[(e - 1) % NSK], ((e - 1) / NSK) & 1, 0x623);
                 if ((agreed = named_or(1, C::ROTALL, !ok))) {
                     ok = false;
                     break;
@@ -718,7 +718,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                 // with four rows per turn the 128K batch took 1130 us instead of 810.)
                 uint32_t f = over_g((uint32_t)(j0 + row0));
                 angles(f, by);
-                if (!ro.wait(&bars.kfull[e % C::NKF], (e / C::NKF) & 1, 0x424)) { ok = false; break; }
+                if (!ro.wait(&bars.kfull[e % C::NKF], (e / C::NKF) & 1, 0x624)) { ok = false; break; }
                 auto advance = [&](int r) {
                     const uint32_t fn = over_g((uint32_t)(j0 + r));
                     if (fn != f) {
@@ -757,7 +757,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             } else {
                 // a request's last tiles: drafted rows sit at their depths (rows past the
                 // end: 0, they are masked)
-                if (!ro.wait(&bars.kfull[e % C::NKF], (e / C::NKF) & 1, 0x424)) { ok = false; break; }
+                if (!ro.wait(&bars.kfull[e % C::NKF], (e / C::NKF) & 1, 0x624)) { ok = false; break; }
 #pragma unroll 1
                 for (int x = 0; x < RPT; ++x) {
                     const int r = row0 + x, j = j0 + r;

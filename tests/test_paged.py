@@ -550,6 +550,37 @@ def test_generation_with_drafts_over_the_paged_cache():
     assert checked > 100
 
 
+@pytest.mark.parametrize("dtype,nodes,codes", [("bf16", 1, (0x601, 0x641)), ("bf16", 8, (0x601, 0x641)),
+                                               # 48, 160 rows a kv head: the kernel for more than 32
+                                               ("bf16", 12, (0x501, 0x641)), ("bf16", 40, (0x501, 0x641)), ("fp32", 1, (0x701, 0x711)),
+                                               ("fp32", 12, (0x701, 0x711))])
+def test_expired_wait_is_reported_and_the_context_recovers(dtype, nodes, codes):
+    """The first key tile is never loaded and every wait is limited to about a
+    millisecond: the launch ends by itself, says so, and leaves nothing behind."""
+    import torch
+    jl.device_status()
+    lens, Hq, Hkv, d = [2000, 700, 5], 8, 2, 128
+    pool = Pool(61, [L + nodes for L in lens], Hkv, d, 64, dtype)
+    N = 3 * nodes
+    q = queries(61, N, Hq, d, dtype)
+    par = random_parents(np.random.default_rng(61), nodes, "random")
+    args = (q, pool.kc, pool.vc, pool.tab, ints(lens), ints([0, nodes, 2 * nodes, N]), ints(par * 3))
+    kw = dict(max_nodes=nodes, w0=64, w_pretrained=400, rope_theta=1e4)
+    before = jl.decode_tree(*args, **kw)
+    jl.device_status()
+    jl.debug_inject_timeout(jl.INJECT_DECODE_COPY, 2_000_000)
+    jl.decode_tree(*args, **kw)
+    with pytest.raises(jl.JetLongError) as ei:
+        jl.device_status()
+    assert ei.value.status == 4, str(ei.value)  # JETLONG_ERR_TIMEOUT
+    msg = str(ei.value)
+    assert codes[0] <= int(msg[msg.index("code 0x") + 5:].split(")")[0], 16) <= codes[1], msg
+    jl.device_status()
+    again = jl.decode_tree(*args, **kw)
+    jl.device_status()
+    assert torch.equal(again, before)
+
+
 def test_captured_step_follows_growing_requests():
     """One decode step (tables, append, attention, lengths) captured once and
     replayed: lengths, tables and pages advance on the device."""
