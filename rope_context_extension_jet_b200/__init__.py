@@ -14,6 +14,7 @@ distance-routed softmax).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -444,6 +445,16 @@ def _need(t, name):
     return t
 
 
+def _on(stream):
+    """Context in which a call's own tensors are made: those of another stream than the
+    current one are allocated on it, so that their memory is free there before the call
+    and is not handed out elsewhere until the call is done with it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(stream)
+
+
 def _caches(kcache, vcache):
     if kcache.dim() != 4 or vcache.shape != kcache.shape:
         raise ValueError("kcache and vcache must both be [num_pages, Hkv, page_size, d]")
@@ -472,12 +483,13 @@ def block_tables(lens, grow, block_table, held, free_list, free_count, *, page_s
         raise ValueError("block_table must be [B, max_pages] and free_list one-dimensional")
     B, max_pages = block_table.shape
     i32, dev = torch.int32, block_table.device
-    lens_out = torch.empty(B, dtype=i32, device=dev) if lens_out is None else lens_out
-    held_out = torch.empty(B, dtype=i32, device=dev) if held_out is None else held_out
-    free_count_out = torch.empty(1, dtype=i32, device=dev) if free_count_out is None else free_count_out
-    slot_map = torch.empty(n_rows, dtype=i32, device=dev) if slot_map is None else slot_map
-    row_start = torch.empty(B + 1, dtype=i32, device=dev) if row_start is None else row_start
-    status = torch.empty(B, dtype=i32, device=dev) if status is None else status
+    with _on(stream):
+        lens_out = torch.empty(B, dtype=i32, device=dev) if lens_out is None else lens_out
+        held_out = torch.empty(B, dtype=i32, device=dev) if held_out is None else held_out
+        free_count_out = torch.empty(1, dtype=i32, device=dev) if free_count_out is None else free_count_out
+        slot_map = torch.empty(n_rows, dtype=i32, device=dev) if slot_map is None else slot_map
+        row_start = torch.empty(B + 1, dtype=i32, device=dev) if row_start is None else row_start
+        status = torch.empty(B, dtype=i32, device=dev) if status is None else status
     lib = load_library()
     cur, raw = _current()
     _check(lib.jetlong_block_tables(
@@ -557,13 +569,14 @@ def decode_tree(q, kcache, vcache, block_table, lens, row_start, parents=None, o
     B, max_pages = block_table.shape
     if row_start is None and N != B:
         raise ValueError("without row_start, q must have one row per request")
-    if out is None:
-        out = torch.empty_like(q)
-    _like(out, q, "out", "q")
     lib = load_library()
-    if workspace is None:
-        workspace = torch.empty(decode_tree_workspace_size(B, Hq, Hkv, d, int(max_nodes)), dtype=torch.uint8,
-                                device=q.device)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = torch.empty(decode_tree_workspace_size(B, Hq, Hkv, d, int(max_nodes)), dtype=torch.uint8,
+                                    device=q.device)
+    _like(out, q, "out", "q")
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     cur, raw = _current()
     _check(lib.jetlong_decode_tree(
@@ -586,8 +599,9 @@ def tree_commit(kcache, vcache, block_table, lens, row_start, parents, last, *, 
     if block_table.dim() != 2 or row_start.dim() != 1:
         raise ValueError("block_table must be [B, max_pages] and row_start [B + 1]")
     B, max_pages = block_table.shape
-    lens_out = torch.empty_like(lens) if lens_out is None else lens_out
-    n_accepted = torch.empty_like(lens) if n_accepted is None else n_accepted
+    with _on(stream):
+        lens_out = torch.empty_like(lens) if lens_out is None else lens_out
+        n_accepted = torch.empty_like(lens) if n_accepted is None else n_accepted
     # without parents (chains) the token rows are not read and need no bound
     N = 2147483647 if parents is None else parents.numel()
     lib = load_library()

@@ -316,6 +316,29 @@ def test_two_streams_with_their_own_workspaces():
 
 
 # ------------------------------------------------------------------ cache_append
+def test_own_tensors_of_a_call_on_another_stream():
+    """Workspaces and results that a call makes for itself belong to the stream it runs
+    on: work of the current stream before and after it does not touch them."""
+    import torch
+    pool = Pool(23, [3000, 200], 2, 128, 64, "bf16")
+    q = queries(23, 2, 8, 128, "bf16")
+    args = (q, pool.kc, pool.vc, pool.tab, ints([2999, 199]))
+    kw = dict(w0=64, w_pretrained=400, rope_theta=1e4)
+    ref = jl.decode_paged(*args, **kw)
+    size = jl.decode_tree_workspace_size(2, 8, 2, 128)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)  # the call starts some 10 ms later
+        out = jl.decode_paged(*args, stream=s, **kw)
+        junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        jl.device_status()
+        assert torch.equal(out, ref)
+        del junk
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("N,Hkv,d,ps", [(0, 2, 64, 16), (1, 1, 64, 16), (5, 3, 128, 32), (1000, 8, 128, 64)])
 @pytest.mark.parametrize("layout", ["plain", "fused", "heads_first"])
