@@ -4,7 +4,8 @@
 // decode_paged.cu, paged_common.cuh; shared roles: paged_tc_roles.cuh).
 //
 //   S [128 rows x 128 keys] = Q_rot [128 x d] K_rot^T      (fp16 operands)
-//   O [128 rows x d]       += P [128 x 128] V              (bf16 operands, P in TMEM)
+//   O [128 rows x d]       += P [128 x 128] V              (bf16 operands, P in TMEM; for
+//                                                           half of the keys as two terms)
 // A softmax thread owns half of a row (64 keys of one TMEM lane), so the running
 // reference, the sum and the rescale factor are its own and no element needs a
 // per-column factor; from about 32 rows on that beats the form of decode_paged_tc.cu,
@@ -19,8 +20,9 @@
 //
 // Warp roles: 0 / 3 producers, 1 MMA issuer, 2 tensor memory and planner, 4-11
 // rotation, 12-15 / 16-19 softmax of the first / second 64 keys of a tile.
-// TMEM (512 columns): S_0, S_1 (128 each; the halves of P_s over columns 0-31 and
-// 64-95 of S_s, each over the half of S_s it was made from), O_0, O_1.
+// TMEM (512 columns): S_0, S_1 (128 each; P_s over S_s, each half over the half it was
+// made from: the weights in columns 0-31, what they leave of 16 bits in 32-47), O_0,
+// O_1.
 #include <algorithm>
 
 #include "paged_tc_roles.cuh"
@@ -64,6 +66,11 @@ __global__ void __launch_bounds__(640, 1)
 {
     using C = RowCfg<D, NROWS>;
     constexpr bool PAIR = NROWS == 256;
+    // 32-key parts of a half whose weights keep 16 bits (split_weights): here, unlike in
+    // decode_paged_tc.cu, each costs a product and the softmax's time.  128K trees of 64
+    // nodes: error 2.4e-3 (rms, of the results) and 1779 us with none, 2.2e-3 and 1939 us
+    // with one of the two, 1.9e-3 and 2238 us with both; rounding the results is 1.6e-3.
+    constexpr int PARTS = 1;
     constexpr int NSK = C::NSK, NSV = C::NSV;
     unsigned char* const smem = smem_base();
     const Role<C> ro(p, ln);
@@ -111,8 +118,11 @@ __global__ void __launch_bounds__(640, 1)
                 tc_fence_after();
                 const uint64_t vd = sdesc_sw128(sb + C::V0 + st * C::TILE, C::ATOM_K, 1024);
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int half = 0; half < 2; ++half) {
                     umma_pv_k64(tm + 256 + s * 128, tm + s * 128 + 64 * half, vd + 512 * half, IPV, pfirst[s] && half == 0 ? 0u : 1u);
+                    for (int part = 0; part < PARTS; ++part)
+                        umma_ts_k32(tm + 256 + s * 128, tm + s * 128 + 64 * half + 32 + 16 * part, vd + 512 * half + 256 * part, IPV);
+                }
                 umma_commit_elect(&pvdone[s]);
                 if (!PAIR || s == 1) umma_commit_elect(&bars.vempty[st]);
                 ++done[s];
@@ -335,19 +345,29 @@ __global__ void __launch_bounds__(640, 1)
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
                     // the stream's last P V finished before this tile's Q K^T (issued later by
                     // the same issuer), so each half of P may go over its half of S
-                    uint32_t pk[KT / 4];
 #pragma unroll
-                    for (int u = 0; u < KT / 2; u += 4) {
-                        const float2 y0 = fma2(make_float2(x[u], x[u + 1]), sl, nm);
-                        const float2 y1 = fma2(make_float2(x[u + 2], x[u + 3]), sl, nm);
-                        const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
-                        const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
-                        acc0 = add2(acc0, p0);
-                        acc1 = add2(acc1, p1);
-                        pk[u >> 1] = pack_bf16x2(p0.x, p0.y);
-                        pk[(u >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
+                    for (int part = 0; part < 2; ++part) {
+                        uint32_t pk[16], rest[16];
+#pragma unroll
+                        for (int u = 0; u < 32; u += 4) {
+                            const float* z = x + 32 * part + u;
+                            const float2 y0 = fma2(make_float2(z[0], z[1]), sl, nm);
+                            const float2 y1 = fma2(make_float2(z[2], z[3]), sl, nm);
+                            const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
+                            const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+                            acc0 = add2(acc0, p0);
+                            acc1 = add2(acc1, p1);
+                            if (part < PARTS) {
+                                pk[u >> 1] = split_weights(p0.x, p0.y, rest[u >> 1]);
+                                pk[(u >> 1) + 1] = split_weights(p1.x, p1.y, rest[(u >> 1) + 1]);
+                            } else {
+                                pk[u >> 1] = pack_bf16x2(p0.x, p0.y);
+                                pk[(u >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
+                            }
+                        }
+                        tmem_st16(s_col + 16 * part, pk);
+                        if (part < PARTS) tmem_st16(s_col + 32 + 16 * part, rest);
                     }
-                    tmem_st32(s_col, pk);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();

@@ -6,7 +6,8 @@
 // 128.  Per tile, with the keys as the 128 rows of the first product so that its
 // cost follows the number of query rows:
 //   S^T [128 keys x RT]  = K_rot [128 x d] Q_rot^T [d x RT]   (fp16 operands)
-//   O^T [d x RT]        += V^T [d x 128] P^T [128 x RT]       (bf16 operands)
+//   O^T [d x RT]        += V^T [d x 128] P^T [128 x RT]       (bf16 operands; P as two
+//                          terms, for which a product of 64 columns has room)
 // both accumulated in fp32 in tensor memory.  A softmax thread owns one key (one
 // TMEM lane) and walks the RT columns, so the weights of a key leave as whole
 // 16-byte chunks; each thread sums its own key's weights.  The running
@@ -37,7 +38,9 @@ template <int D, int NCOL>
 struct CfgTiles {
     static constexpr int DIM = D, ROWS = NCOL;
     static constexpr int NSK = D == 64 ? 6 : 3, NSV = D == 64 ? 4 : 2;  // 16 / 32 KB stages
-    static constexpr int NPV = 64;      // columns of the second product (one swizzle atom is 64 wide)
+    // columns of the second product (one swizzle atom is 64 wide): the weights' upper
+    // bits from 0 on, the rest of them from 32 on
+    static constexpr int NPV = 64, REST = 32;
     static constexpr int NP = 2;        // P buffers
     static constexpr int THREADS = 512;
     // the two rotation warpgroups take tiles in turn (one's latencies under the
@@ -337,11 +340,14 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
                         for (int c = 0; c < NCOL; c += 16) {
                             if (c >= cols) break;
                             uint32_t o[16];
-                            tmem_ld16(tl + 2 * TS + c, o);
-                            tmem_wait_ld();
+#pragma unroll 1
+                            for (int at = c; at < C::NPV; at += C::REST) {
+                                tmem_ld16(tl + 2 * TS + at, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha[c + x]);
-                            tmem_st16(tl + 2 * TS + c, o);
+                                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha[c + x]);
+                                tmem_st16(tl + 2 * TS + at, o);
+                            }
                         }
                         tmem_wait_st();
                     }
@@ -360,16 +366,17 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < NCOL; c += 8) {
                         if ((c & ~15) < cols) {
-                            uint32_t o[4];
+                            uint32_t o[4], rest[4];
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const float a = ex2_approx(y[c + 2 * x]), b = ex2_approx(y[c + 2 * x + 1]);
                                 l[c + 2 * x] += a;
                                 l[c + 2 * x + 1] += b;
-                                o[x] = pack_bf16x2(a, b);
+                                o[x] = split_weights(a, b, rest[x]);
                             }
-                            *reinterpret_cast<uint4*>(pb + (((((c) & 63) >> 3) ^ (key & 7)) << 4)) =
-                                make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(pb + (((c >> 3) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(pb + ((((c + C::REST) >> 3) ^ (key & 7)) << 4)) =
+                                make_uint4(rest[0], rest[1], rest[2], rest[3]);
                         }
                     }
                 }
@@ -408,13 +415,14 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
 #pragma unroll
             for (int cb = 0; cb < NCOL; cb += 16) {
                 if (cb >= cols) break;
-                uint32_t o[16];
+                uint32_t o[16], rest[16];
                 tmem_ld16(tl + 2 * TS + cb, o);
+                tmem_ld16(tl + 2 * TS + C::REST + cb, rest);
                 tmem_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
                     const int row = __shfl_sync(0xffffffffu, to, cb + x);
-                    const float val = __uint_as_float(o[x]) * __shfl_sync(0xffffffffu, inv, cb + x);
+                    const float val = (__uint_as_float(o[x]) + __uint_as_float(rest[x])) * __shfl_sync(0xffffffffu, inv, cb + x);
                     if (key < D && cb + x < cols) {
                         if (whole)
                             orow[(size_t)row * D] = __float2bfloat16_rn(val);
