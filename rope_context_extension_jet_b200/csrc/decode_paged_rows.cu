@@ -23,6 +23,10 @@
 // TMEM (512 columns): S_0, S_1 (128 each; P_s over S_s, each half over the half it was
 // made from: the weights in columns 0-31, what they leave of 16 bits in 32-47), O_0,
 // O_1.
+//
+// Bound: the softmax (8 x 32K rows: 16 nodes 253 us, 64 nodes 476 us; 64 nodes at 8 x
+// 128K 1.86-1.94 ms, where bytes and products each take 0.66 ms).  Exponentials on the
+// FMA pipes made it slower (an eighth of them 6%): instruction issue, not MUFU, is short.
 #include <algorithm>
 
 #include "paged_tc_roles.cuh"
