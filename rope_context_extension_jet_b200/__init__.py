@@ -411,15 +411,23 @@ def decode_noalloc(q, kcache, vcache, L: int, out=None, *, w0: int, w_pretrained
 # step (block_tables, cache_append, decode_paged or decode_tree, tree_commit) can
 # be captured into a CUDA graph.
 
+#
+# The host side of a call is as long as a small call itself, so it asks for little:
+# torch is looked up once, devices and streams by the raw queries (the public ones
+# build objects), each tensor for its type, shape, device and layout.
+_torch = None
+
+
 def _current():
-    """(current device, its current stream's handle): looked up once per call, by the
-    raw queries (the public ones build objects, at a few microseconds a call, and a
-    decode step is a few microseconds long)."""
-    import torch
-    if not torch.cuda.is_initialized():
+    """(current device, its current stream's handle)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if not _torch.cuda.is_initialized():
         return -2, None  # then no tensor is on a device either: the argument checks say so
-    dev = torch._C._cuda_getDevice()
-    return dev, torch._C._cuda_getCurrentRawStream(dev)
+    dev = _torch._C._cuda_getDevice()
+    return dev, _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _ptr(t, name, dev):
@@ -431,12 +439,13 @@ def _ptr(t, name, dev):
 
 def _ints(t, name, shape, dev):
     """Device pointer of an int32 array of the given shape (None stays None)."""
-    import torch
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != shape:
+    if t.dtype is not _torch.int32 or t.shape != shape:
         raise ValueError(f"{name} must be an int32 tensor of shape {tuple(shape)} (got {t.dtype}, {tuple(t.shape)})")
-    return _ptr(t, name, dev)
+    if t.get_device() != dev or not t.is_contiguous():
+        return _dev(t, name)
+    return t.data_ptr()
 
 
 def _need(t, name):
@@ -482,24 +491,24 @@ def block_tables(lens, grow, block_table, held, free_list, free_count, *, page_s
     if block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("block_table must be [B, max_pages] and free_list one-dimensional")
     B, max_pages = block_table.shape
-    i32, dev = torch.int32, block_table.device
-    with _on(stream):
-        lens_out = torch.empty(B, dtype=i32, device=dev) if lens_out is None else lens_out
-        held_out = torch.empty(B, dtype=i32, device=dev) if held_out is None else held_out
-        free_count_out = torch.empty(1, dtype=i32, device=dev) if free_count_out is None else free_count_out
-        slot_map = torch.empty(n_rows, dtype=i32, device=dev) if slot_map is None else slot_map
-        row_start = torch.empty(B + 1, dtype=i32, device=dev) if row_start is None else row_start
-        status = torch.empty(B, dtype=i32, device=dev) if status is None else status
-    lib = load_library()
+    made = (lens_out, held_out, free_count_out, slot_map, row_start, status)
+    sizes = [n if x is None else 0 for x, n in zip(made, (B, B, 1, n_rows, B + 1, B))]
+    if any(sizes) or slot_map is None:
+        with _on(stream):  # one allocation for all that the caller did not bring
+            new = torch.empty(sum(sizes), dtype=torch.int32, device=block_table.device).split(sizes)
+        lens_out, held_out, free_count_out, slot_map, row_start, status = \
+            [y if x is None else x for x, y in zip(made, new)]
+    lib = _lib or load_library()
     cur, raw = _current()
+    reqs, one = (B,), (1,)
     _check(lib.jetlong_block_tables(
-        _ints(_need(lens, "lens"), "lens", (B,), cur), _ints(_need(grow, "grow"), "grow", (B,), cur),
-        _ints(release, "release", (B,), cur), _ints(_need(held, "held"), "held", (B,), cur),
-        _ints(_need(free_count, "free_count"), "free_count", (1,), cur), _ints(block_table, "block_table", (B, max_pages), cur),
-        _ints(free_list, "free_list", free_list.shape, cur), _ints(lens_out, "lens_out", (B,), cur),
-        _ints(held_out, "held_out", (B,), cur), _ints(free_count_out, "free_count_out", (1,), cur),
+        _ints(_need(lens, "lens"), "lens", reqs, cur), _ints(_need(grow, "grow"), "grow", reqs, cur),
+        _ints(release, "release", reqs, cur), _ints(_need(held, "held"), "held", reqs, cur),
+        _ints(_need(free_count, "free_count"), "free_count", one, cur), _ints(block_table, "block_table", (B, max_pages), cur),
+        _ints(free_list, "free_list", free_list.shape, cur), _ints(lens_out, "lens_out", reqs, cur),
+        _ints(held_out, "held_out", reqs, cur), _ints(free_count_out, "free_count_out", one, cur),
         _ints(slot_map, "slot_map", (n_rows,), cur), _ints(row_start, "row_start", (B + 1,), cur),
-        _ints(status, "status", (B,), cur), B, max_pages, int(page_size), int(num_pages), free_list.shape[0], int(n_rows),
+        _ints(status, "status", reqs, cur), B, max_pages, int(page_size), int(num_pages), free_list.shape[0], int(n_rows),
         raw if stream is None else stream.cuda_stream), lib)
     return BlockTables(lens_out, held_out, free_count_out, slot_map, row_start, status)
 
@@ -523,7 +532,7 @@ def cache_append(k, v, slot_map, kcache, vcache, stream=None):
     slots of the paged cache; slot -1 leaves a row out (jetlong_cache_append)."""
     num_pages, Hkv, page_size, d = _caches(kcache, vcache)
     N = k.shape[0]
-    lib = load_library()
+    lib = _lib or load_library()
     cur, raw = _current()
     kp, kt, kh = _rows(k, "k", kcache, N, cur)
     vp, vt, vh = _rows(v, "v", kcache, N, cur)
@@ -569,7 +578,7 @@ def decode_tree(q, kcache, vcache, block_table, lens, row_start, parents=None, o
     B, max_pages = block_table.shape
     if row_start is None and N != B:
         raise ValueError("without row_start, q must have one row per request")
-    lib = load_library()
+    lib = _lib or load_library()
     with _on(stream):
         if out is None:
             out = torch.empty_like(q)
@@ -604,7 +613,7 @@ def tree_commit(kcache, vcache, block_table, lens, row_start, parents, last, *, 
         n_accepted = torch.empty_like(lens) if n_accepted is None else n_accepted
     # without parents (chains) the token rows are not read and need no bound
     N = 2147483647 if parents is None else parents.numel()
-    lib = load_library()
+    lib = _lib or load_library()
     cur, raw = _current()
     _check(lib.jetlong_tree_commit(
         _ptr(kcache, "kcache", cur), _ptr(vcache, "vcache", cur), _ints(block_table, "block_table", (B, max_pages), cur),
