@@ -489,11 +489,17 @@ cudaError_t run_one(const PagedProblem& p, const Launch& ln, cudaStream_t st, in
     int nsm = 0;
     e = once.get(&nsm, [&](int* n, int dev) {
         cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncAttributes a;
+        if (err == cudaSuccess) err = cudaFuncGetAttributes(&a, kern);
+        // fewer registers at launch would leave setmaxnreg waiting
+        using C = RowCfg<D, NROWS>;
+        if (err == cudaSuccess && a.numRegs * C::THREADS < (C::R_PROD + 2 * C::R_ROT + 2 * C::R_SOFT) * 128)
+            err = cudaErrorInvalidKernelImage;
         return err == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : err;
     });
     if (e != cudaSuccess) return e;
     *grid = std::min(nsm, kTcCtas);
-    kern<<<*grid, 640, smem, st>>>(tk, tv, p, ln);
+    kern<<<*grid, RowCfg<D, NROWS>::THREADS, smem, st>>>(tk, tv, p, ln);
     return cudaGetLastError();
 }
 

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
 }  // namespace
 
 // One CTA where latency is all (B = 16, 16 rows: 4.8 us); else a cluster of eight (of
-// 1024 threads each the 41,000 rows took 19.4 us).
+// 1024 threads each the 35,000 rows took 19.4 us).
 cudaError_t launch_block_tables(const TablesProblem& p, cudaStream_t s, int* nlaunch)
 {
     static PerDevice once;
