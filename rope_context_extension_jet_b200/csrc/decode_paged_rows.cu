@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(640, 1)
     // nodes: error 2.4e-3 (rms, of the results) and 1779 us with none, 2.2e-3 and 1939 us
     // with one of the two, 1.9e-3 and 2238 us with both; rounding the results is 1.6e-3.
     constexpr int PARTS = 1;
+    constexpr float kSumMax = 65536.f;  // 2^kExceed
+    static_assert(kExceed == 16.f && PARTS == 1, "weights");
     constexpr int NSK = C::NSK, NSV = C::NSV;
     unsigned char* const smem = smem_base();
     const Role<C> ro(p, ln);
@@ -235,133 +237,134 @@ __global__ void __launch_bounds__(640, 1)
                     for (int w = 0; w < C::ROT / 32; ++w) any_scaled |= flags[w];
                     const bool drafted = j0 + KT > L || have != all_pages;
                     const bool masked = drafted || (g == 0 ? j0 <= near : j0 > far);
-                    float x[KT / 2];
-                    {
-                        uint32_t t0[32], t1[32];
-                        tmem_ld32(s_col, t0);
-                        tmem_ld32(s_col + 32, t1);
-                        tmem_wait_ld();
+                    uint32_t pk[KT / 4], rest[16 * PARTS];
+                    float sum;
+                    // Weights at the reference as it is.  If they sum to 2^kExceed at most, no
+                    // logit passed it by kExceed; else some row's reference moves and the
+                    // scores are read once more.  (With the row's largest logit taken first
+                    // on every tile, 64 nodes at 8 x 128K took 2.00 ms instead of 1.69.)
+                    bool moved = tasks < 2;  // a stream's first tile sets its reference
+#pragma unroll 1
+                    for (;;) {
+                        float x[KT / 2];
+                        {
+                            uint32_t t0[32], t1[32];
+                            tmem_ld32(s_col, t0);
+                            tmem_ld32(s_col + 32, t1);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) {
-                            x[u] = __uint_as_float(t0[u]);
-                            x[32 + u] = __uint_as_float(t1[u]);
+                            for (int u = 0; u < 32; ++u) {
+                                x[u] = __uint_as_float(t0[u]);
+                                x[32 + u] = __uint_as_float(t1[u]);
+                            }
                         }
-                    }
-                    // key rows that were scaled by a power of two (paged_tc_roles.cuh) scaled back
-                    if (any_scaled) {
-                        asm volatile("" ::: "memory");
-                        const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT + h * 64);
+                        // key rows that were scaled by a power of two (paged_tc_roles.cuh) scaled back
+                        if (any_scaled) {
+                            asm volatile("" ::: "memory");
+                            const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT + h * 64);
+#pragma unroll
+                            for (int u = 0; u < KT / 2; u += 4) {
+                                const float4 f = k4[u / 4];
+                                x[u] *= f.x;
+                                x[u + 1] *= f.y;
+                                x[u + 2] *= f.z;
+                                x[u + 3] *= f.w;
+                            }
+                        }
+                        // what does not belong to this row and item at -inf
+                        if (masked) {
+                            asm volatile("" ::: "memory");  // a branch, not predication: most tiles skip this
+                            const int row = (PAIR ? s * 128 : 0) + lrow, k0 = j0 + h * 64;  // first key of the half
+                            const int lim = reinterpret_cast<const int*>(un + C::U_LIM)[row];
+                            const int G = reinterpret_cast<const int*>(un + C::U_QG)[row];
+                            // committed keys: those past the border (exact phase) or up to it
+                            // (remote phase of this row's group size), before row L
+                            const int cut = lim < k0 ? 0 : lim - k0 + 1;  // keys [0, cut) of the half are remote
+                            const int c0 = L - k0;                        // keys [0, c0) are committed
+                            auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+                            unsigned long long keep = below(cut);
+                            keep = g == 0 ? ~keep : (G == g ? keep : 0ull);
+                            keep &= below(c0);
+                            if (drafted) {
+                                const unsigned long long anc = ancs[PAIR ? s * 128 : 0];
+                                unsigned long long nodes = 0;  // drafted nodes this row attends in this phase
+#pragma unroll 1
+                                for (int v = 0; v < T; ++v) {
+                                    const bool local = L + depth[v] > lim;
+                                    const bool in = g == 0 ? local : (!local && G == g);
+                                    nodes |= (unsigned long long)(in && ((anc >> v) & 1)) << v;
+                                }
+                                // node v is key c0 + v
+                                if (c0 > -64 && c0 < 64) keep |= c0 >= 0 ? nodes << c0 : nodes >> -c0;
+                                if (have != all_pages) {
+                                    unsigned long long there = 0;
+#pragma unroll 1
+                                    for (int u = 0; u < 64; ++u) there |= (unsigned long long)((have >> ((h * 64 + u) >> gshift)) & 1u) << u;
+                                    keep &= there;
+                                }
+                            }
+                            const uint32_t b0 = (uint32_t)keep, b1 = (uint32_t)(keep >> 32);
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) {
+                                x[u] = (b0 >> u) & 1 ? x[u] : -INFINITY;
+                                x[32 + u] = (b1 >> u) & 1 ? x[32 + u] : -INFINITY;
+                            }
+                            __syncwarp();
+                        }
+                        if (moved) {
+                            asm volatile("" ::: "memory");
+                            float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                            for (int u = 4; u < KT / 2; u += 8) {
+                                m4[0] = fmax3(m4[0], x[u], x[u + 1]);
+                                m4[1] = fmax3(m4[1], x[u + 2], x[u + 3]);
+                                if (u + 4 < KT / 2) {
+                                    m4[2] = fmax3(m4[2], x[u + 4], x[u + 5]);
+                                    m4[3] = fmax3(m4[3], x[u + 6], x[u + 7]);
+                                }
+                            }
+                            const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            // logits in log2 units: x cq, cq > 0 a power of two times the scale;
+                            // both halves of the row's keys follow
+                            tops[h * 128 + lrow] = top;
+                            named_sync(pid, 64);
+                            const float mt = fmaxf(top, tops[(h ^ 1) * 128 + lrow]) * cq;
+                            // (64 weights that sum to more than 2^kExceed hold one above 2^(kExceed - 6))
+                            const bool resc = mt > ref + (kExceed - 6.5f);
+                            float alpha = 1.f;
+                            if (resc) {
+                                alpha = ex2_approx(ref - (mt + kAbove));
+                                ref = mt + kAbove;
+                                l *= alpha;
+                            }
+                            // O (a half of its columns each) follows before any of this tile's P is published
+                            if (tasks > 1 && __any_sync(0xffffffffu, resc)) {
+                                ok = ro.wait(&pvdone[s], (done - 1) & 1, 0x533);
+                                tc_fence_after();
+                                const uint32_t o_col = lanes + 256 + s * 128 + h * (D / 2);
+#pragma unroll 1
+                                for (int cc = 0; cc < D / 2; cc += 16) {
+                                    uint32_t tt[16];
+                                    tmem_ld16(o_col + cc, tt);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int u = 0; u < 16; ++u) tt[u] = __float_as_uint(__uint_as_float(tt[u]) * alpha);
+                                    tmem_st16(o_col + cc, tt);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                        const float2 sl = make_float2(cq, cq), nm = make_float2(-ref, -ref);
+                        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int u = 0; u < KT / 2; u += 4) {
-                            const float4 f = k4[u / 4];
-                            x[u] *= f.x;
-                            x[u + 1] *= f.y;
-                            x[u + 2] *= f.z;
-                            x[u + 3] *= f.w;
-                        }
-                    }
-                    // what does not belong to this row and item at -inf
-                    if (masked) {
-                        asm volatile("" ::: "memory");  // a branch, not predication: most tiles skip this
-                        const int row = (PAIR ? s * 128 : 0) + lrow, k0 = j0 + h * 64;  // first key of the half
-                        const int lim = reinterpret_cast<const int*>(un + C::U_LIM)[row];
-                        const int G = reinterpret_cast<const int*>(un + C::U_QG)[row];
-                        // committed keys: those past the border (exact phase) or up to it
-                        // (remote phase of this row's group size), before row L
-                        const int cut = lim < k0 ? 0 : lim - k0 + 1;  // keys [0, cut) of the half are remote
-                        const int c0 = L - k0;                        // keys [0, c0) are committed
-                        auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
-                        unsigned long long keep = below(cut);
-                        keep = g == 0 ? ~keep : (G == g ? keep : 0ull);
-                        keep &= below(c0);
-                        if (drafted) {
-                            const unsigned long long anc = ancs[PAIR ? s * 128 : 0];
-                            unsigned long long nodes = 0;  // drafted nodes this row attends in this phase
-#pragma unroll 1
-                            for (int v = 0; v < T; ++v) {
-                                const bool local = L + depth[v] > lim;
-                                const bool in = g == 0 ? local : (!local && G == g);
-                                nodes |= (unsigned long long)(in && ((anc >> v) & 1)) << v;
-                            }
-                            // node v is key c0 + v
-                            if (c0 > -64 && c0 < 64) keep |= c0 >= 0 ? nodes << c0 : nodes >> -c0;
-                            if (have != all_pages) {
-                                unsigned long long there = 0;
-#pragma unroll 1
-                                for (int u = 0; u < 64; ++u) there |= (unsigned long long)((have >> ((h * 64 + u) >> gshift)) & 1u) << u;
-                                keep &= there;
-                            }
-                        }
-                        const uint32_t b0 = (uint32_t)keep, b1 = (uint32_t)(keep >> 32);
-#pragma unroll
-                        for (int u = 0; u < 32; ++u) {
-                            x[u] = (b0 >> u) & 1 ? x[u] : -INFINITY;
-                            x[32 + u] = (b1 >> u) & 1 ? x[32 + u] : -INFINITY;
-                        }
-                        __syncwarp();
-                    }
-                    float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int u = 4; u < KT / 2; u += 8) {
-                        m4[0] = fmax3(m4[0], x[u], x[u + 1]);
-                        m4[1] = fmax3(m4[1], x[u + 2], x[u + 3]);
-                        if (u + 4 < KT / 2) {
-                            m4[2] = fmax3(m4[2], x[u + 4], x[u + 5]);
-                            m4[3] = fmax3(m4[3], x[u + 6], x[u + 7]);
-                        }
-                    }
-                    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    // logits in log2 units: x cq, cq > 0 a power of two times the scale
-                    if (named_or(pid, 64, top * cq > ref + kExceed || !ok)) {
-                        // some row's reference moves: both halves of its keys follow
-                        asm volatile("" ::: "memory");
-                        tops[h * 128 + lrow] = top;
-                        if (named_or(pid, 64, !ok)) {
-                            alive = false;
-                            break;
-                        }
-                        const float mt = fmaxf(top, tops[(h ^ 1) * 128 + lrow]) * cq;
-                        const bool resc = mt > ref + kExceed;
-                        float alpha = 1.f;
-                        if (resc) {
-                            alpha = ex2_approx(ref - (mt + kAbove));
-                            ref = mt + kAbove;
-                            l *= alpha;
-                        }
-                        // O (a half of its columns each) follows before any of this tile's P is published
-                        if (tasks > 1 && __any_sync(0xffffffffu, resc)) {
-                            ok = ro.wait(&pvdone[s], (done - 1) & 1, 0x533);
-                            tc_fence_after();
-                            const uint32_t o_col = lanes + 256 + s * 128 + h * (D / 2);
-#pragma unroll 1
-                            for (int cc = 0; cc < D / 2; cc += 16) {
-                                uint32_t tt[16];
-                                tmem_ld16(o_col + cc, tt);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) tt[u] = __float_as_uint(__uint_as_float(tt[u]) * alpha);
-                                tmem_st16(o_col + cc, tt);
-                            }
-                            tmem_wait_st();
-                        }
-                    }
-                    const float2 sl = make_float2(cq, cq), nm = make_float2(-ref, -ref);
-                    float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-                    // the stream's last P V finished before this tile's Q K^T (issued later by
-                    // the same issuer), so each half of P may go over its half of S
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        uint32_t pk[16], rest[16];
-#pragma unroll
-                        for (int u = 0; u < 32; u += 4) {
-                            const float* z = x + 32 * part + u;
-                            const float2 y0 = fma2(make_float2(z[0], z[1]), sl, nm);
-                            const float2 y1 = fma2(make_float2(z[2], z[3]), sl, nm);
+                            const float2 y0 = fma2(make_float2(x[u], x[u + 1]), sl, nm);
+                            const float2 y1 = fma2(make_float2(x[u + 2], x[u + 3]), sl, nm);
                             const float2 p0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
                             const float2 p1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
                             acc0 = add2(acc0, p0);
                             acc1 = add2(acc1, p1);
-                            if (part < PARTS) {
+                            if (u < 32 * PARTS) {
                                 pk[u >> 1] = split_weights(p0.x, p0.y, rest[u >> 1]);
                                 pk[(u >> 1) + 1] = split_weights(p1.x, p1.y, rest[(u >> 1) + 1]);
                             } else {
@@ -369,14 +372,24 @@ __global__ void __launch_bounds__(640, 1)
                                 pk[(u >> 1) + 1] = pack_bf16x2(p1.x, p1.y);
                             }
                         }
-                        tmem_st16(s_col + 16 * part, pk);
-                        if (part < PARTS) tmem_st16(s_col + 32 + 16 * part, rest);
+                        sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                        if (moved || !named_or(pid, 64, !(sum <= kSumMax) || !ok)) break;
+                        if (named_or(pid, 64, !ok)) {
+                            alive = false;
+                            break;
+                        }
+                        moved = true;
                     }
+                    if (!alive) break;
+                    // the stream's last P V finished before this tile's Q K^T (issued later by
+                    // the same issuer), so each half of P may go over its half of S
+                    tmem_st32(s_col, pk);
+                    tmem_st16(s_col + 32, rest);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&pfull[s]);
-                    l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                    l += sum;
                     ++done;
                     ++tasks;
                     swap_streams();
