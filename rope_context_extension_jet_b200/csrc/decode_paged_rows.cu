@@ -24,8 +24,8 @@
 // made from: the weights in columns 0-31, what they leave of 16 bits in 32-47), O_0,
 // O_1.
 //
-// Bound: the softmax (8 x 32K rows: 16 nodes 253 us, 64 nodes 476 us; 64 nodes at 8 x
-// 128K 1.86-1.94 ms, where bytes and products each take 0.66 ms).  Exponentials on the
+// Bound: the softmax (8 x 32K rows: 16 nodes 247 us, 64 nodes 451 us; 64 nodes at 8 x
+// 128K 1.67-1.78 ms, where bytes and products each take 0.66 ms).  Exponentials on the
 // FMA pipes made it slower (an eighth of them 6%): instruction issue, not MUFU, is short.
 #include <algorithm>
 
@@ -72,8 +72,9 @@ __global__ void __launch_bounds__(640, 1)
     constexpr bool PAIR = NROWS == 256;
     // 32-key parts of a half whose weights keep 16 bits (split_weights): here, unlike in
     // decode_paged_tc.cu, each costs a product and the softmax's time.  128K trees of 64
-    // nodes: error 2.4e-3 (rms, of the results) and 1779 us with none, 2.2e-3 and 1939 us
-    // with one of the two, 1.9e-3 and 2238 us with both; rounding the results is 1.6e-3.
+    // nodes, with the row maximum still taken on every tile: error 2.4e-3 (rms, of the
+    // results) and 1779 us with none, 2.2e-3 and 1939 us with one of the two, 1.9e-3 and
+    // 2238 us with both; rounding the results alone is 1.6e-3.
     constexpr int PARTS = 1;
     constexpr float kSumMax = 65536.f;  // 2^kExceed
     static_assert(kExceed == 16.f && PARTS == 1, "weights");
