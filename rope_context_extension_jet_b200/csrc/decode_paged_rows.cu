@@ -53,8 +53,8 @@ template <int D, int NROWS>
 struct RowCfg : RowTiles<D, NROWS>,
                 Notes<D, NROWS, RowTiles<D, NROWS>::NSK, RowTiles<D, NROWS>::NSV, RowTiles<D, NROWS>::BASE, 6, 20> {
     static constexpr int XCH = RowCfg::NOTES_END;  // [2][128] sums of both streams over a half's keys
-    static constexpr int TOP = XCH + 2 * 128 * 8;  // [2][128] largest logit of a half's keys
-    static constexpr int TOTAL = TOP + 2 * 128 * 4 + 1024;
+    static constexpr int TOP = XCH + 2 * 128 * 8;  // [2][2][128] largest logit of a half's keys, per stream
+    static constexpr int TOTAL = TOP + 2 * 2 * 128 * 4 + 1024;
     static_assert(TOTAL <= 232448, "shared memory");
     // Registers per thread after setmaxnreg: producers / issuer / planner, the two
     // rotation and the two softmax warpgroups.  640 threads launch with 96 each, and an
@@ -326,10 +326,15 @@ __global__ void __launch_bounds__(640, 1)
                             }
                             const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                             // logits in log2 units: x cq, cq > 0 a power of two times the scale;
-                            // both halves of the row's keys follow
-                            tops[h * 128 + lrow] = top;
+                            // both halves of the row's keys follow.  One place per stream: a
+                            // unit's first two tasks come here without an agreement between them,
+                            // so the other warp may already write the second task's maximum while
+                            // this one reads the first's.  (From the third on, the agreement that
+                            // ends a task's first pass lies between a read and the next write.)
+                            float* const mine = tops + (s * 2 + h) * 128 + lrow;
+                            *mine = top;
                             named_sync(pid, 64);
-                            const float mt = fmaxf(top, tops[(h ^ 1) * 128 + lrow]) * cq;
+                            const float mt = fmaxf(top, mine[h ? -128 : 128]) * cq;
                             // (64 weights that sum to more than 2^kExceed hold one above 2^(kExceed - 6))
                             const bool resc = mt > ref + (kExceed - 6.5f);
                             float alpha = 1.f;
