@@ -40,7 +40,8 @@
  *   - All pointers named d_* or tensor pointers are DEVICE memory owned by the
  *     caller (jetlong_prefill_streamed also takes host buffers, named *_host).
  *     The library never writes q, k, v or the caches (jetlong_prefill_streamed
- *     fills the device staging buffers it is given) and allocates no device
+ *     fills the device staging buffers it is given; jetlong_cache_append and
+ *     jetlong_tree_commit write the paged cache) and allocates no device
  *     memory in any call.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  *     stream) on the current device.
@@ -245,6 +246,10 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  *                   request;
  *   lens            int32 [B]: committed rows of each request.  Row r sits at
  *                   position r.
+ * Entries behind a request's pages may hold anything, or JETLONG_NO_PAGE, which
+ * jetlong_block_tables writes where it has refused pages: the other calls leave out
+ * a request whose last new row has this entry, so that a refused request passes
+ * through the rest of the step untouched.
  * One step: jetlong_block_tables makes room for each request's new rows and gives
  * their slots, jetlong_cache_append writes the rows, jetlong_decode_paged (one new
  * row per request) or jetlong_decode_tree (a tree of drafted rows) attends, and
@@ -257,6 +262,8 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  * JETLONG_ERR_INVALID_ARG (and clears the record).  int32 arrays must be 4-byte
  * aligned, caches and rows 16-byte. */
 
+#define JETLONG_NO_PAGE (-2)
+
 /* Block tables and slot maps from request lengths.  Request b holds held[b]
  * pages (entries [0, held[b]) of its table row) for its lens[b] rows and takes
  * grow[b] >= 0 more rows.  With release (may be NULL) and release[b] != 0 the
@@ -268,7 +275,10 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  *   status[b]     0 granted; 1 refused, the free pages end here (a request that
  *                 needs pages and comes after one is refused as well; one that
  *                 needs none is granted); 2 refused, longer than its table row.
- *                 A refused request keeps its pages;
+ *                 A refused request keeps its pages, and the entries that its new
+ *                 rows needed besides become JETLONG_NO_PAGE (status 2: the table
+ *                 row ends before them; the other calls leave the request out as
+ *                 well and report its length);
  *   lens_out[b]   lens[b], or 0 if released (the new rows are not counted);
  *   held_out[b], *free_count_out, block_table entries [held, held_out);
  *   row_start     [B + 1]: first of each request's rows in the step's token rows
@@ -300,7 +310,7 @@ int jetlong_cache_append(const void* k, const void* v, const int32_t* slot_map, 
  * caller has appended request b's new row as row lens[b]; it is the query's own
  * row, at position lens[b], and G follows lens[b] + 1 (jetlong_decode with L =
  * lens[b] + 1, each request with its own length).  A request with lens[b] < 0 is
- * idle: its row of out is left as it was.  workspace: at least
+ * idle, and a refused one is left out: their rows of out are left as they were.  workspace: at least
  * jetlong_decode_tree_workspace_size(B, Hq, Hkv, d, 1) bytes; its contents on
  * entry do not matter, and calls that share it must not overlap on the device. */
 int jetlong_decode_paged(const void* q, const void* kcache, const void* vcache, void* out, const int32_t* block_table,
@@ -317,8 +327,8 @@ int jetlong_decode_paged(const void* q, const void* kcache, const void* vcache, 
  * attends the committed rows and its ancestors and itself, at their positions
  * -- what jetlong_decode gives after its path has been committed.
  * Values in rows a node does not attend (non-finite ones too) do not reach it.
- * Requests may have no nodes; token rows outside every request are left as they
- * were.  Without row_start (NULL) every request has one node, row b:
+ * Requests may have no nodes; token rows outside every request, and those of
+ * refused requests, are left as they were.  Without row_start (NULL) every request has one node, row b:
  * jetlong_decode_paged.
  * Two launches: the attention, cut into equal pieces over all requests whatever
  * their lengths, and a merge of the cut ones.  bf16 takes the input range of
@@ -335,7 +345,7 @@ int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, v
  * .. lens[b] + n - 1 (row lens[b] + path[j] is copied to row lens[b] + j; raw rows
  * need no new rotation), lens_out[b] = lens[b] + n (lens_out may be lens) and,
  * unless NULL, n_accepted[b] = n.  The remaining drafted rows are left where they
- * are, behind the new length.  row_start, parents, N, max_nodes as in
+ * are, behind the new length.  Of a refused request nothing is committed (n = 0).  row_start, parents, N, max_nodes as in
  * jetlong_decode_tree. */
 int jetlong_tree_commit(void* kcache, void* vcache, const int32_t* block_table, const int32_t* lens,
                         const int32_t* row_start, const int32_t* parents, const int32_t* last, int32_t* lens_out,

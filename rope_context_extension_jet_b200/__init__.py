@@ -28,7 +28,7 @@ __all__ = [
     "DECODE_NOALLOC_SCRATCH_BYTES", "selftest_wait_timeout", "debug_inject_timeout",
     "INJECT_PREFILL_KEY_TILE", "INJECT_DECODE_COPY", "debug_rope_phase", "debug_tile_plan", "debug_ex2", "debug_rope_keys",
     "BlockTables", "block_tables", "cache_append", "decode_tree_workspace_size", "decode_paged", "decode_tree",
-    "tree_commit",
+    "tree_commit", "NO_PAGE",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +36,7 @@ LIB_PATH = os.path.join(_PKG, "libjetlong.so")
 
 BF16 = 0
 FP32 = 1
+NO_PAGE = -2  # block table entry of rows that block_tables refused
 _STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT"}
 
 _lock = threading.Lock()
@@ -478,7 +479,7 @@ class BlockTables(NamedTuple):
     free_count: "object"  # [1] free pages left
     slot_map: "object"    # [n_rows] slot of every new row, -1: none
     row_start: "object"   # [B + 1] first token row of each request
-    status: "object"      # [B] 0 granted, 1 no free pages, 2 longer than its table row
+    status: "object"      # [B] 0 granted, 1 no free pages, 2 longer than its table row (both: left out by the other calls)
 
 
 def block_tables(lens, grow, block_table, held, free_list, free_count, *, page_size: int, num_pages: int, n_rows: int,

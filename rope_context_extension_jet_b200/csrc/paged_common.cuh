@@ -15,6 +15,8 @@
 
 namespace jl {
 
+constexpr int kNoPage = JETLONG_NO_PAGE;  // table entry of rows that block_tables refused
+
 constexpr int kMaxNodes = 64;  // drafted tokens per request: ancestors fit one 64-bit mask
 
 constexpr int kMaxTableRequests = 8192;  // block_tables: 5 words of shared memory per request
@@ -140,6 +142,14 @@ struct SeqPlan {
     int row_tiles;
 };
 
+// The request's rows up to `row` were refused their pages: its table holds no page for
+// the last of them.  (What a refused request's table held there before, some other
+// request's page perhaps, is not attended or written.)
+__device__ __forceinline__ bool no_room(const int* table, int b, int max_pages, int page_shift, int row)
+{
+    return __ldg(table + (size_t)b * max_pages + (row >> page_shift)) == kNoPage;
+}
+
 // Largest depth of a tree (a parent that does not precede its node counts as -1).
 __device__ inline int tree_depth(const int* parents, int T)
 {
@@ -172,6 +182,8 @@ __device__ inline SeqPlan seq_plan(const PagedProblem& p, int b, bool report)
     if (T > 0 && (long long)L + T > (long long)p.max_pages * p.page_size) bad = kBadLength;
     if (bad) {
         if (report) record_input(p.input_error, bad);
+        T = 0;
+    } else if (T > 0 && no_room(p.table, b, p.max_pages, p.page_shift, L + T - 1)) {
         T = 0;
     }
     s.L = L;

@@ -100,14 +100,14 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, gtid = cta * TB_NT + tid, gthr = gridDim.x * TB_NT;
 
-    // For every x in [0, total), b the last index with sum[b] <= x: *to = value(*from, off)
-    // of the Move f(x, b); to = null: nothing.  BATCH of them side by side: their
+    // For every x in [first, total), b the last index with sum[b] <= x: *to = value(*from,
+    // off) of the Move f(x, b); to = null: nothing.  BATCH of them side by side: their
     // bisections and their loads overlap.
-    auto each = [&](int total, const int* sum, auto f, auto value) {
+    auto each = [&](int first, int total, const int* sum, auto f, auto value) {
         constexpr int BATCH = 4;
         const int top = 1 << (31 - __clz(p.B));  // largest power of two <= B
 #pragma unroll 1
-        for (long long x0 = gtid; x0 < total; x0 += (long long)BATCH * gthr) {
+        for (long long x0 = (long long)first + gtid; x0 < total; x0 += (long long)BATCH * gthr) {
             Move m[BATCH];
             int b[BATCH];
             bool in[BATCH];
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
     // handed out together and given back together restore the list's order
     const auto as_is = [](int page, int) { return page; };
     if ((long long)count + carry.back > p.free_cap && gtid == 0) record_input(p.input_error, kBadFreeList);
-    each(carry.back, s_back, [&](int x, int b) {
+    each(0, carry.back, s_back, [&](int x, int b) {
         const long long at = (long long)count + (carry.back - s_back[b + 1]) + (s_back[b + 1] - 1 - x);
         return Move{p.table + (size_t)b * p.max_pages + (x - s_back[b]), at < p.free_cap ? p.free_list + at : nullptr, 0};
     }, as_is);
@@ -198,9 +198,13 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
     // a request is granted if the running sum up to it fits; the sums ascend, so
     // the pages handed out are the largest sum that fits
     const int granted = s_need[bisect(s_need, p.B + 1, avail)];
-    each(granted, s_need, [&](int x, int b) {
+    each(0, granted, s_need, [&](int x, int b) {
         return Move{p.free_list + (avail - 1 - x), p.table + (size_t)b * p.max_pages + s_held[b] + (x - s_need[b]), 0};
     }, as_is);
+    // the sums behind it are those of refused requests: their tables say so
+    each(granted, s_need[p.B], s_need, [&](int x, int b) {
+        return Move{nullptr, p.table + (size_t)b * p.max_pages + s_held[b] + (x - s_need[b]), 0};
+    }, [](int, int) { return kNoPage; });
     for (int b = gtid; b < p.B; b += gthr) {
         const int need = s_need[b + 1] - s_need[b];
         const bool too_long = s_held[b] & kLong, refused = need > 0 && s_need[b + 1] > avail;
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
         *p.free_count_out = avail - granted;
     }
     const int rows = min(p.n_rows, s_row[p.B]);
-    each(rows, s_row, [&](int n, int b) {
+    each(0, rows, s_row, [&](int n, int b) {
         const int held = s_held[b], need = s_need[b], need1 = s_need[b + 1], pos = s_len[b] + (n - s_row[b]);
         const int c = pos >> p.page_shift;
         const int* from = c < held ? p.table + (size_t)b * p.max_pages + c : p.free_list + (avail - 1 - (need + c - held));

@@ -1,0 +1,139 @@
+"""Requests that take no part in a step of the paged cache: refused ones, idle
+places, requests whose numbers are out of range.  Nothing of theirs is written, and
+nobody else's rows are read for them or written by them."""
+import numpy as np
+import pytest
+
+import paged_reference as R
+import rope_context_extension_jet_b200 as jl
+from test_paged import dt, ints, random_parents, starts_of, to64
+
+pytestmark = pytest.mark.gpu
+
+HQ, HKV, D, PS = 8, 2, 64, 16
+KW = dict(w0=24, w_pretrained=40, rope_theta=1e4)
+
+
+def bits(t):
+    import torch
+    return t.view(torch.int16 if t.element_size() == 2 else torch.int32)
+
+
+class Server:
+    """A pool of pages and the requests on it; the host keeps every row it has committed."""
+
+    def __init__(self, B, wide, pages, dtype="bf16", seed=1, free=None):
+        import torch
+        self.g = np.random.default_rng(seed)
+        self.kc = torch.full((pages, HKV, PS, D), float("nan"), dtype=dt(dtype), device="cuda")
+        self.vc = torch.full_like(self.kc, float("nan"))
+        free = self.g.permutation(pages) if free is None else free
+        self.free, self.count = ints(list(free) + [0] * (pages - len(free))), ints([len(free)])
+        self.table, self.held, self.lens = ints(np.zeros((B, wide))), ints([0] * B), ints([0] * B)
+        self.B, self.pages, self.dtype = B, pages, dtype
+        self.rows = [([], []) for _ in range(B)]
+
+    def randn(self, *shape):
+        import torch
+        return torch.from_numpy(self.g.standard_normal(shape, dtype=np.float32)).cuda().to(dt(self.dtype))
+
+    def tables(self, grow, release=None):
+        return jl.block_tables(self.lens, ints(grow), self.table, self.held, self.free, self.count, page_size=PS,
+                               num_pages=self.pages, n_rows=max(0, sum(max(0, x) for x in grow)),
+                               release=None if release is None else ints(release), lens_out=self.lens, held_out=self.held,
+                               free_count_out=self.count)
+
+    def step(self, nodes, last, release=None, kind="chain", report=None):
+        """One whole step, checked against the rows the host has kept.  Returns (status, out)."""
+        import torch
+        par = [random_parents(self.g, n, kind) for n in nodes]
+        flat = ints([x for p in par for x in p])
+        N = sum(nodes)
+        q, k, v = self.randn(N, HQ, D), self.randn(N, HKV, D), self.randn(N, HKV, D)
+        out = torch.full_like(q, 7.5)
+        before = [self.lens.tolist(), bits(self.kc).clone(), bits(self.vc).clone()]
+        r = self.tables(nodes, release)
+        if release is not None:
+            for b in range(self.B):
+                if release[b]:
+                    self.rows[b] = ([], [])
+        status, lens = r.status.tolist(), self.lens.tolist()
+        jl.cache_append(k, v, r.slot_map, self.kc, self.vc)
+        mid = bits(self.kc).clone(), bits(self.vc).clone()
+        jl.decode_tree(q, self.kc, self.vc, self.table, self.lens, r.row_start, flat, out, max_nodes=64, **KW)
+        _, acc = jl.tree_commit(self.kc, self.vc, self.table, self.lens, r.row_start, flat, ints(last), max_nodes=64,
+                                lens_out=self.lens)
+        if report:
+            with pytest.raises(jl.JetLongError, match=report):
+                jl.device_status()
+        jl.device_status()
+        want_k, want_v = mid[0].clone(), mid[1].clone()
+        at, table = 0, self.table.tolist()
+        for b, n in enumerate(nodes):
+            if status[b]:
+                assert (out[at:at + n] == 7.5).all(), ("rows of a refused request were written", b)
+                assert int(acc[b]) == 0 and int(self.lens[b]) == before[0][b]
+            else:
+                L, path, x = lens[b], [], last[b]
+                while x >= 0:
+                    path.append(x)
+                    x = par[b][x]
+                path.reverse()
+                if n:
+                    own = [torch.stack(self.rows[b][i] + list((k, v)[i][at:at + n])) for i in range(2)]  # [L + n, HKV, D]
+                    k64, v64 = (to64(x)[:, :, None] for x in own)  # pages of one row
+                    ref, tol = R.attend(to64(q[at:at + n]), k64, v64, list(range(L + n)), L, par[b], w0=KW["w0"],
+                                        w_pre=KW["w_pretrained"], theta=KW["rope_theta"], scale=D ** -0.5, dtype=self.dtype)
+                    assert (np.abs(to64(out[at:at + n]) - ref) <= tol).all(), b
+                assert int(acc[b]) == len(path) and int(self.lens[b]) == L + len(path)
+                for j, x in enumerate(path):
+                    self.rows[b][0].append(k[at + x])
+                    self.rows[b][1].append(v[at + x])
+                    for want, old in ((want_k, mid[0]), (want_v, mid[1])):
+                        s, t = L + x, L + j
+                        want[table[b][t // PS], :, t % PS] = old[table[b][s // PS], :, s % PS]
+            at += n
+        # the commit has moved what it should and nothing else
+        assert torch.equal(bits(self.kc), want_k) and torch.equal(bits(self.vc), want_v)
+        return status, out
+
+
+# ------------------------------------------------------------------ refused
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("grow", [12, 60])
+def test_refused_requests_stay_out_of_the_whole_step(dtype, grow):
+    """The free pages end in the middle of a batch.  The table rows of the refused requests
+    hold other requests' pages behind their own: those are neither attended nor written, and
+    once pages are free again the request goes on where it was."""
+    s = Server(4, 8, 12, dtype)
+    s.table.copy_(ints([[s.g.integers(0, 12) for _ in range(8)] for _ in range(4)]))
+    assert s.step([30, 14, 31, 10], [29, 13, 30, 9])[0] == [0, 0, 0, 0]     # 2 + 1 + 2 + 1 pages; 6 left
+    assert s.step([50, grow, 20, 3], [49, grow - 1, 19, 2])[0] == [0, 0 if grow == 12 else 1, 0 if grow == 12 else 1, 0]
+    if grow == 12:                                                          # 3 + 1 + 2: none left
+        assert s.step([3, 9, 20, 2], [2, 8, 19, 1], kind="random")[0] == [1, 1, 1, 0]
+    else:                                                                   # 3 left
+        assert s.step([0, 60, 1, 60], [-1, 59, 0, 59], kind="random")[0] == [0, 1, 0, 1]
+        assert s.step([5, 64, 60, 3], [4, 63, 59, 2], kind="star")[0][1:3] == [1, 1]
+    assert s.step([0, 9, 2, 1], [-1, 8, 1, 0], release=[1, 0, 0, 0], kind="comb")[0] == [0, 0, 0, 0]
+    s.step([20, 4, 6, 9], [11, 3, 5, 8], kind="random")
+
+
+def test_a_refused_request_in_decode_paged():
+    import torch
+    s = Server(3, 4, 4)
+    assert s.step([16, 32, 5], [15, 31, 4])[0] == [0, 0, 0]
+    s.table[0, 1:] = s.table[1, 0]
+    r = s.tables([1, 1, 1])
+    assert r.status.tolist() == [1, 1, 0] and r.slot_map.tolist()[:2] == [-1, -1]
+    q, k, v = s.randn(3, HQ, D), s.randn(3, HKV, D), s.randn(3, HKV, D)
+    jl.cache_append(k, v, r.slot_map, s.kc, s.vc)
+    out = jl.decode_paged(q, s.kc, s.vc, s.table, s.lens, torch.full_like(q, 7.5), **KW)
+    jl.device_status()
+    assert (out[:2] == 7.5).all() and (out[2] != 7.5).all()
+
+
+def test_a_request_longer_than_its_table_stays_out_and_is_reported():
+    s = Server(2, 2, 8)
+    assert s.step([30, 9], [29, 8])[0] == [0, 0]
+    assert s.step([3, 2], [2, 1], report="length")[0] == [2, 0]
+    assert s.step([2, 2], [1, 1])[0] == [0, 0]
