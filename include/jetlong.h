@@ -345,7 +345,8 @@ int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, v
  * .. lens[b] + n - 1 (row lens[b] + path[j] is copied to row lens[b] + j; raw rows
  * need no new rotation), lens_out[b] = lens[b] + n (lens_out may be lens) and,
  * unless NULL, n_accepted[b] = n.  The remaining drafted rows are left where they
- * are, behind the new length.  Of a refused request nothing is committed (n = 0).  row_start, parents, N, max_nodes as in
+ * are, behind the new length.  Nothing of a refused request, or of one with a
+ * value out of range, is committed (n = 0).  row_start, parents, N, max_nodes as in
  * jetlong_decode_tree. */
 int jetlong_tree_commit(void* kcache, void* vcache, const int32_t* block_table, const int32_t* lens,
                         const int32_t* row_start, const int32_t* parents, const int32_t* last, int32_t* lens_out,

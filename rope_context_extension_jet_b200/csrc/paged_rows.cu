@@ -54,11 +54,12 @@ constexpr int CM_NT = 512;
 // len + path[j] to len + j.  path[j] >= j, so with one thread moving a given
 // 16-byte column of all path rows in order, no row is overwritten before it is read: a row
 // below the current one is never read again, and loads of a group of rows come
-// before its stores.
+// before its stores.  A request is committed whole or not at all: with a parent or a
+// page out of range nothing of it moves and its length stays.
 __global__ void __launch_bounds__(CM_NT) tree_commit_kernel(CommitProblem p)
 {
     __shared__ int s_par[kMaxNodes], s_n;
-    __shared__ long long s_src[kMaxNodes], s_dst[kMaxNodes];  // row offsets of kv head 0, -1: page out of range
+    __shared__ long long s_src[kMaxNodes], s_dst[kMaxNodes];  // row offsets of kv head 0; source -1: stays where it is
     const int b = blockIdx.x, tid = threadIdx.x;
     const int L = p.lens[b];
     const int a = p.row_start[b];
@@ -72,18 +73,17 @@ __global__ void __launch_bounds__(CM_NT) tree_commit_kernel(CommitProblem p)
         T = 0;
         last = -1;
     }
+    bool wrong = false;
     if (tid < T) {
         int x = tid - 1;
         if (p.parents) {
             x = p.parents[a + tid];
-            if (x < -1 || x >= tid) {
-                record_input(p.input_error, kBadParent);
-                x = -1;
-            }
+            wrong = x < -1 || x >= tid;
+            if (wrong) record_input(p.input_error, kBadParent);
         }
         s_par[tid] = x;
     }
-    __syncthreads();
+    if (__syncthreads_or(wrong)) last = -1;
     if (tid == 0) {
         unsigned long long m = 0;
         for (int x = last; x >= 0; x = s_par[x]) m |= 1ull << x;
@@ -92,18 +92,20 @@ __global__ void __launch_bounds__(CM_NT) tree_commit_kernel(CommitProblem p)
         s_n = n;
     }
     __syncthreads();
-    const int n = s_n;
+    int n = s_n;
+    wrong = false;
     if (tid < n) {
         const int from = L + s_par[tid], to = L + tid;
         const int fp = p.table[(size_t)b * p.max_pages + (from >> p.page_shift)];
         const int tp = p.table[(size_t)b * p.max_pages + (to >> p.page_shift)];
         const bool ok = (unsigned)fp < (unsigned)p.num_pages && (unsigned)tp < (unsigned)p.num_pages;
-        if (!ok) record_input(p.input_error, kBadPage);
+        wrong = !ok;
+        if (wrong) record_input(p.input_error, kBadPage);
         s_src[tid] = ok && from != to
                          ? ((long long)fp * p.Hkv * p.page_size + (from & (p.page_size - 1))) * p.row_bytes : -1;
         s_dst[tid] = ((long long)tp * p.Hkv * p.page_size + (to & (p.page_size - 1))) * p.row_bytes;
     }
-    __syncthreads();
+    if (__syncthreads_or(wrong)) n = 0;
     const int cpr = p.row_bytes >> 4, cols = p.Hkv * cpr * 2;
     for (int c = tid; c < cols; c += CM_NT) {
         const int h = (c / cpr) % p.Hkv;
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(CM_NT) tree_commit_kernel(CommitProblem p)
         }
     }
     if (tid == 0) {
-        p.lens_out[b] = L + n;  // L of a refused request comes out as it went in
+        p.lens_out[b] = L + n;  // L of a request left out comes out as it went in
         if (p.n_accepted) p.n_accepted[b] = n;
     }
 }

@@ -137,3 +137,40 @@ def test_a_request_longer_than_its_table_stays_out_and_is_reported():
     assert s.step([30, 9], [29, 8])[0] == [0, 0]
     assert s.step([3, 2], [2, 1], report="length")[0] == [2, 0]
     assert s.step([2, 2], [1, 1])[0] == [0, 0]
+
+
+# ------------------------------------------------------------------ out of range
+@pytest.mark.parametrize("page", [-1, 50, 2 ** 31 - 1, -2 ** 31])
+def test_commit_leaves_out_a_request_with_a_bad_page(page):
+    """Rows that cannot be moved are not committed: the request stays as it was."""
+    import torch
+    s = Server(3, 4, 10)
+    assert s.step([14, 30, 20], [13, 29, 19])[0] == [0] * 3
+    r = s.tables([9, 6, 3])
+    k, v = s.randn(18, HKV, D), s.randn(18, HKV, D)
+    jl.cache_append(k, v, r.slot_map, s.kc, s.vc)
+    par = ints([-1, 0, 0, 1, 1, 3, 3, 5, 5] + [-1, 0, 0, 0, 0, 0] + [-1, 0, 1])
+    s.table[0, 1] = page
+    before = bits(s.kc).clone(), bits(s.vc).clone()
+    n, acc = jl.tree_commit(s.kc, s.vc, s.table, s.lens, r.row_start, par, ints([8, -1, -1]), max_nodes=9)
+    with pytest.raises(jl.JetLongError, match="page number"):
+        jl.device_status()
+    assert n.tolist() == [14, 30, 20] and acc.tolist() == [0, 0, 0]
+    assert torch.equal(bits(s.kc), before[0]) and torch.equal(bits(s.vc), before[1])
+
+
+def test_commit_leaves_out_a_request_with_a_bad_parent():
+    import torch
+    s = Server(2, 4, 10)
+    assert s.step([14, 30], [13, 29])[0] == [0, 0]
+    r = s.tables([5, 4])
+    k, v = s.randn(9, HKV, D), s.randn(9, HKV, D)
+    jl.cache_append(k, v, r.slot_map, s.kc, s.vc)
+    for x in (2, 3, -2, 2 ** 31 - 1, -2 ** 31):  # of node 2
+        before = bits(s.kc).clone(), bits(s.vc).clone()
+        n, acc = jl.tree_commit(s.kc, s.vc, s.table, s.lens, r.row_start, ints([-1, 0, x, 2, 3] + [-1, 0, 1, 2]), ints([4, 3]),
+                                max_nodes=9)
+        with pytest.raises(jl.JetLongError, match="parent"):
+            jl.device_status()
+        assert n.tolist() == [14, 34] and acc.tolist() == [0, 4]
+        assert torch.equal(bits(s.kc), before[0]) and torch.equal(bits(s.vc), before[1])  # (a chain's rows stay in place)
