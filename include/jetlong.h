@@ -245,7 +245,8 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  *                   rows [p page_size, (p + 1) page_size); a page belongs to one
  *                   request;
  *   lens            int32 [B]: committed rows of each request.  Row r sits at
- *                   position r.
+ *                   position r.  A negative length marks an idle place: without
+ *                   new rows it passes through every call as it is.
  * Entries behind a request's pages may hold anything, or JETLONG_NO_PAGE, which
  * jetlong_block_tables writes where it has refused pages: the other calls leave out
  * a request whose last new row has this entry, so that a refused request passes
@@ -266,8 +267,12 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
 
 /* Block tables and slot maps from request lengths.  Request b holds held[b]
  * pages (entries [0, held[b]) of its table row) for its lens[b] rows and takes
- * grow[b] >= 0 more rows.  With release (may be NULL) and release[b] != 0 the
- * request first gives all its pages back and starts again from length 0.
+ * grow[b] >= 0 more rows (an idle place none).  With release (may be NULL) and
+ * release[b] != 0 the request first gives all its pages back and starts again from
+ * length 0, whatever lens[b] was; an idle place that is released and takes no rows
+ * stays idle.  (A released request without new rows has length 0 and no page: its
+ * length is to be made negative before jetlong_decode_paged, which would take row 0
+ * for its new row.)
  * free_list[0 .. *free_count) are the free pages (room for free_cap); pages are
  * taken from its end, in request order.  Pages given back by this call go onto
  * the list first (last request first, its last page first) and can be taken by
@@ -279,7 +284,8 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  *                 rows needed besides become JETLONG_NO_PAGE (status 2: the table
  *                 row ends before them; the other calls leave the request out as
  *                 well and report its length);
- *   lens_out[b]   lens[b], or 0 if released (the new rows are not counted);
+ *   lens_out[b]   lens[b], or 0 if released (the new rows are not counted); an
+ *                 idle place's own;
  *   held_out[b], *free_count_out, block_table entries [held, held_out);
  *   row_start     [B + 1]: first of each request's rows in the step's token rows
  *                 (the running sum of grow, refused requests included);
@@ -345,9 +351,9 @@ int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, v
  * .. lens[b] + n - 1 (row lens[b] + path[j] is copied to row lens[b] + j; raw rows
  * need no new rotation), lens_out[b] = lens[b] + n (lens_out may be lens) and,
  * unless NULL, n_accepted[b] = n.  The remaining drafted rows are left where they
- * are, behind the new length.  Nothing of a refused request, or of one with a
- * value out of range, is committed (n = 0).  row_start, parents, N, max_nodes as in
- * jetlong_decode_tree. */
+ * are, behind the new length.  An idle place without nodes passes through.  Nothing
+ * of a refused request, or of one with a value out of range, is committed (n = 0).
+ * row_start, parents, N, max_nodes as in jetlong_decode_tree. */
 int jetlong_tree_commit(void* kcache, void* vcache, const int32_t* block_table, const int32_t* lens,
                         const int32_t* row_start, const int32_t* parents, const int32_t* last, int32_t* lens_out,
                         int32_t* n_accepted, int B, int N, int Hkv, int d, int num_pages, int page_size, int max_pages,

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(CM_NT) tree_commit_kernel(CommitProblem p)
     int T = p.row_start[b + 1] - a, last = p.last[b];
     int bad = 0;
     if (a < 0 || T < 0 || T > p.max_nodes || a > p.N - T) bad = kBadRows;
-    else if (L < 0 || (long long)L + T > (long long)p.max_pages * p.page_size) bad = kBadLength;
+    else if (T > 0 && (L < 0 || (long long)L + T > (long long)p.max_pages * p.page_size)) bad = kBadLength;
     else if (last < -1 || last >= T) bad = kBadParent;
     if (bad && tid == 0) record_input(p.input_error, bad);
     if (bad || (T > 0 && no_room(p.table, b, p.max_pages, p.page_shift, L + T - 1))) {

@@ -47,15 +47,23 @@ __device__ __forceinline__ Req load_req(const TablesProblem& p, int b, bool repo
     r.grow = p.grow[b];
     r.held = p.held[b];
     r.back = 0;
-    if (r.len < 0 || r.grow < 0 || r.held < 0 || r.held > p.max_pages) {
+    const bool released = p.release && p.release[b] != 0;
+    const bool idle = r.len < 0 && r.grow == 0;  // keeps its length, released or not
+    if ((r.len < 0 && !idle && !released) || r.grow < 0 || r.held < 0 || r.held > p.max_pages) {
         if (report) record_input(p.input_error, kBadLength);
-        r.len = max(r.len, 0);
+        if (!idle) r.len = max(r.len, 0);
         r.grow = max(r.grow, 0);
         r.held = min(max(r.held, 0), p.max_pages);
     }
-    if (p.release && p.release[b] != 0) {
+    if (released) {
         r.back = r.held;
-        r.len = r.held = 0;
+        r.held = 0;
+        if (!idle) r.len = 0;
+    }
+    if (idle) {
+        r.need = 0;
+        r.too_long = false;
+        return r;
     }
     const long long pages = ((long long)r.len + r.grow + p.page_size - 1) >> p.page_shift;
     r.need = 0;

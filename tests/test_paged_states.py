@@ -139,6 +139,118 @@ def test_a_request_longer_than_its_table_stays_out_and_is_reported():
     assert s.step([2, 2], [1, 1])[0] == [0, 0]
 
 
+def test_captured_step_with_trees_refusals_and_idle_places():
+    """Tables, append, tree attention and commit captured once and replayed.  The pool is too
+    small: requests are refused and go on when others release their pages; places are idle,
+    and filled again."""
+    import torch
+    g = np.random.default_rng(5)
+    B, wide, T, steps = 5, 6, 6, 40
+    s = Server(B, wide, 5, seed=6)
+    s.table.copy_(ints(g.integers(0, 5, (B, wide))))
+    N = B * T
+    grow, release, last, flat = ints([0] * B), ints([0] * B), ints([-1] * B), ints([-1] * N)
+    q, k, v = s.randn(N, HQ, D), s.randn(N, HKV, D), s.randn(N, HKV, D)
+    out, acc = torch.zeros_like(q), ints([0] * B)
+    bufs = dict(slot_map=ints([0] * N), row_start=ints([0] * (B + 1)), status=ints([0] * B))
+    ws = torch.empty(jl.decode_tree_workspace_size(B, HQ, HKV, D, T), dtype=torch.uint8, device="cuda")
+
+    def step():
+        r = jl.block_tables(s.lens, grow, s.table, s.held, s.free, s.count, page_size=PS, num_pages=s.pages, n_rows=N,
+                            release=release, lens_out=s.lens, held_out=s.held, free_count_out=s.count, **bufs)
+        jl.cache_append(k, v, r.slot_map, s.kc, s.vc)
+        jl.decode_tree(q, s.kc, s.vc, s.table, s.lens, r.row_start, flat, out, max_nodes=T, workspace=ws, **KW)
+        jl.tree_commit(s.kc, s.vc, s.table, s.lens, r.row_start, flat, last, max_nodes=T, lens_out=s.lens, n_accepted=acc)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    seen = {"refused": 0, "idle": 0, "granted": 0}
+    idle = [False] * B
+    for n in range(steps):
+        nodes, rel = [int(x) for x in g.integers(0, T + 1, B)], [0] * B
+        lens = s.lens.tolist()
+        for b in range(B):
+            if idle[b]:
+                if g.random() < 0.4:  # a new request in this place
+                    idle[b], rel[b], nodes[b] = False, 1, max(1, nodes[b])
+                else:
+                    nodes[b] = 0
+            elif lens[b] > 60 or g.random() < 0.05:
+                idle[b], nodes[b], rel[b] = True, 0, 1
+                lens[b] = -1
+            if rel[b]:
+                s.rows[b] = ([], [])
+        s.lens.copy_(ints(lens))
+        par = [random_parents(g, x, "random") for x in nodes]
+        lst = [int(g.integers(-1, x)) if x else -1 for x in nodes]
+        at = starts_of(nodes)
+        flat.copy_(ints([x for p in par for x in p] + [-1] * (N - at[-1])))
+        for t, x in ((grow, nodes), (release, rel), (last, lst)):
+            t.copy_(ints(x))
+        for t in (q, k, v):
+            t.copy_(s.randn(*t.shape))
+        out.fill_(7.5)
+        graph.replay()
+        jl.device_status()
+        status, now = bufs["status"].tolist(), s.lens.tolist()
+        assert (out[at[-1]:] == 7.5).all()
+        for b in range(B):
+            L, rows = 0 if rel[b] and not idle[b] else lens[b], slice(at[b], at[b + 1])
+            if idle[b]:
+                assert now[b] == -1 and status[b] == 0 and int(acc[b]) == 0
+                seen["idle"] += 1
+                continue
+            if status[b]:
+                assert status[b] == 1 and now[b] == L and int(acc[b]) == 0 and (out[rows] == 7.5).all(), (n, b)
+                seen["refused"] += 1
+                continue
+            path, x = [], lst[b]
+            while x >= 0:
+                path.append(x)
+                x = par[b][x]
+            assert now[b] == L + len(path) and int(acc[b]) == len(path) and L == len(s.rows[b][0]), (n, b)
+            if nodes[b]:
+                own = [torch.stack(s.rows[b][i] + list((k, v)[i][rows])) for i in range(2)]
+                ref, tol = R.attend(to64(q[rows]), *(to64(x)[:, :, None] for x in own), list(range(L + nodes[b])), L, par[b],
+                                    w0=KW["w0"], w_pre=KW["w_pretrained"], theta=KW["rope_theta"], scale=D ** -0.5, dtype="bf16")
+                assert (np.abs(to64(out[rows]) - ref) <= tol).all(), (n, b)
+                seen["granted"] += 1
+            for x in reversed(path):
+                s.rows[b][0].append(k[at[b] + x].clone())
+                s.rows[b][1].append(v[at[b] + x].clone())
+    assert min(seen.values()) > 10, seen
+    del graph
+
+
+# ------------------------------------------------------------------ idle
+@pytest.mark.parametrize("in_place", [True, False])
+def test_idle_places_pass_through_a_step(in_place):
+    """lens[b] < 0 and no new rows: the place keeps its length (and its pages, unless it
+    releases them), and no call reports it."""
+    import torch
+    s = Server(4, 4, 10)
+    assert s.step([20, 3, 18, 7], [19, 2, 17, 6])[0] == [0] * 4
+    s.lens[1], s.lens[2] = -1, -7
+    lens = s.lens.clone()
+    out = dict(lens_out=s.lens, held_out=s.held, free_count_out=s.count) if in_place else {}
+    r = jl.block_tables(s.lens, ints([1, 0, 0, 1]), s.table, s.held, s.free, s.count, page_size=PS, num_pages=s.pages, n_rows=2,
+                        release=ints([0, 0, 1, 0]), **out)
+    jl.device_status()
+    assert r.lens.tolist() == lens.tolist() and r.status.tolist() == [0] * 4 and r.row_start.tolist() == [0, 1, 1, 1, 2]
+    assert r.held.tolist() == [2, 1, 0, 1] and int(r.free_count) == 10 - 4
+    q = s.randn(4, HQ, D)
+    o = jl.decode_paged(q, s.kc, s.vc, s.table, r.lens, torch.full_like(q, 7.5), **KW)
+    n, acc = jl.tree_commit(s.kc, s.vc, s.table, r.lens, r.row_start, None, ints([0, -1, -1, 0]), max_nodes=1)
+    jl.device_status()
+    assert (o[1:3] == 7.5).all() and n.tolist() == [21, -1, -7, 8] and acc.tolist() == [1, 0, 0, 1]
+
+
 # ------------------------------------------------------------------ out of range
 @pytest.mark.parametrize("page", [-1, 50, 2 ** 31 - 1, -2 ** 31])
 def test_commit_leaves_out_a_request_with_a_bad_page(page):
