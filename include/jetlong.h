@@ -259,9 +259,9 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  * and replayed as the requests grow.
  *
  * The host cannot check device arrays.  The kernels do: a value out of range is
- * never followed, and the next jetlong_device_status returns
- * JETLONG_ERR_INVALID_ARG (and clears the record).  int32 arrays must be 4-byte
- * aligned, caches and rows 16-byte. */
+ * never followed, its request or row is left out, and the next
+ * jetlong_device_status returns JETLONG_ERR_INVALID_ARG (and clears the record).
+ * int32 arrays must be 4-byte aligned, caches and rows 16-byte. */
 
 #define JETLONG_NO_PAGE (-2)
 
@@ -283,12 +283,17 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  *                 A refused request keeps its pages, and the entries that its new
  *                 rows needed besides become JETLONG_NO_PAGE (status 2: the table
  *                 row ends before them; the other calls leave the request out as
- *                 well and report its length);
+ *                 well and report its length); 3 left out, its lens, grow or held
+ *                 is out of range: its length, its pages and its table row stay
+ *                 (but the entry of its last new row, if it lies in a page behind
+ *                 the committed rows, becomes JETLONG_NO_PAGE), nothing is given
+ *                 back, and device_status reports it;
  *   lens_out[b]   lens[b], or 0 if released (the new rows are not counted); an
  *                 idle place's own;
  *   held_out[b], *free_count_out, block_table entries [held, held_out);
  *   row_start     [B + 1]: first of each request's rows in the step's token rows
- *                 (the running sum of grow, refused requests included);
+ *                 (the running sum of grow, or of 0 where that is negative, refused
+ *                 requests included);
  *   slot_map      [n_rows]: page * page_size + offset of every token row; -1 for
  *                 refused requests and for rows from row_start[B] on.  n_rows
  *                 must be at least row_start[B]; later rows are not written and

@@ -479,7 +479,7 @@ class BlockTables(NamedTuple):
     free_count: "object"  # [1] free pages left
     slot_map: "object"    # [n_rows] slot of every new row, -1: none
     row_start: "object"   # [B + 1] first token row of each request
-    status: "object"      # [B] 0 granted, 1 no free pages, 2 longer than its table row (both: left out by the other calls)
+    status: "object"      # [B] 0 granted, 1 no free pages, 2 longer than its table row (both: left out by the other calls), 3 out of range
 
 
 def block_tables(lens, grow, block_table, held, free_list, free_count, *, page_size: int, num_pages: int, n_rows: int,

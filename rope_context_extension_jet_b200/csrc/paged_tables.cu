@@ -26,7 +26,9 @@ namespace {
 
 constexpr int TB_NT = 512;
 constexpr int kSmallRows = 4 * TB_NT;  // new rows that one CTA handles alone
-constexpr int kLong = 1 << 30;  // flag beside a page count: counts stay below 2^27
+// flags beside a page count (counts stay below 2^27): longer than its table row; numbers
+// out of range, left as it is
+constexpr int kLong = 1 << 30, kBad = 1 << 29;
 
 struct Sum3 {
     long long rows;
@@ -37,7 +39,7 @@ __device__ __forceinline__ Sum3 add3(const Sum3& a, const Sum3& b) { return {a.r
 
 struct Req {
     int len, grow, held, back, need;
-    bool too_long;
+    bool too_long, bad;
 };
 
 __device__ __forceinline__ Req load_req(const TablesProblem& p, int b, bool report)
@@ -48,25 +50,23 @@ __device__ __forceinline__ Req load_req(const TablesProblem& p, int b, bool repo
     r.held = p.held[b];
     r.back = 0;
     const bool released = p.release && p.release[b] != 0;
+    r.need = 0;
+    r.too_long = false;
     const bool idle = r.len < 0 && r.grow == 0;  // keeps its length, released or not
-    if ((r.len < 0 && !idle && !released) || r.grow < 0 || r.held < 0 || r.held > p.max_pages) {
+    r.bad = (r.len < 0 && !idle && !released) || r.grow < 0 || r.held < 0 || r.held > p.max_pages;
+    if (r.bad) {
         if (report) record_input(p.input_error, kBadLength);
-        if (!idle) r.len = max(r.len, 0);
-        r.grow = max(r.grow, 0);
-        r.held = min(max(r.held, 0), p.max_pages);
+        r.grow = max(r.grow, 0);  // its token rows are counted
+        r.held = 0;
+        return r;
     }
     if (released) {
         r.back = r.held;
         r.held = 0;
         if (!idle) r.len = 0;
     }
-    if (idle) {
-        r.need = 0;
-        r.too_long = false;
-        return r;
-    }
+    if (idle) return r;
     const long long pages = ((long long)r.len + r.grow + p.page_size - 1) >> p.page_shift;
-    r.need = 0;
     r.too_long = pages > p.max_pages;
     if (!r.too_long) r.need = max(0, (int)pages - r.held);
     return r;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
 {
     // per request, read once before anything is written: running sums of rows,
     // pages needed and pages given back, rows held and pages held (both 0 once
-    // released; a request longer than its table has kLong set)
+    // released; kLong and kBad mark the requests that take no part)
     extern __shared__ int sm[];
     int* s_row = sm;
     int* s_need = s_row + p.B + 1;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
             const Req r = load_req(p, b, cta == 0);
             x = {r.grow, r.need, r.back};
             s_len[b] = r.len;
-            s_held[b] = r.held | (r.too_long ? kLong : 0);
+            s_held[b] = r.held | (r.too_long ? kLong : 0) | (r.bad ? kBad : 0);
         }
         Sum3 incl = x;
 #pragma unroll
@@ -216,10 +216,16 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
     for (int b = gtid; b < p.B; b += gthr) {
         const int need = s_need[b + 1] - s_need[b];
         const bool too_long = s_held[b] & kLong, refused = need > 0 && s_need[b + 1] > avail;
-        p.status[b] = too_long ? 2 : (refused ? 1 : 0);
+        const bool bad = s_held[b] & kBad;
+        p.status[b] = bad ? 3 : too_long ? 2 : (refused ? 1 : 0);
         p.lens_out[b] = s_len[b];
-        p.held_out[b] = (s_held[b] & ~kLong) + (refused ? 0 : need);
+        p.held_out[b] = bad ? p.held[b] : (s_held[b] & ~kLong) + (refused ? 0 : need);
         p.row_start[b] = s_row[b];
+        if (bad && s_len[b] >= 0 && p.grow[b] > 0) {
+            // what the table holds behind the committed rows is not to be followed either
+            const int c = (int)(((long long)s_len[b] + p.grow[b] - 1) >> p.page_shift);
+            if (c < p.max_pages && c > (s_len[b] - 1) >> p.page_shift) p.table[(size_t)b * p.max_pages + c] = kNoPage;
+        }
     }
     if (gtid == 0) {
         p.row_start[p.B] = s_row[p.B];
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
         const int held = s_held[b], need = s_need[b], need1 = s_need[b + 1], pos = s_len[b] + (n - s_row[b]);
         const int c = pos >> p.page_shift;
         const int* from = c < held ? p.table + (size_t)b * p.max_pages + c : p.free_list + (avail - 1 - (need + c - held));
-        if ((held & kLong) || (need1 > avail && need1 > need)) from = nullptr;  // too long, or refused
+        if ((held & (kLong | kBad)) || (need1 > avail && need1 > need)) from = nullptr;  // takes no part, or refused
         return Move{from, p.slot_map + n, from ? pos & (p.page_size - 1) : -1};
     }, [&](int page, int off) {
         if (off < 0) return -1;

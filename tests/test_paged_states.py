@@ -252,6 +252,58 @@ def test_idle_places_pass_through_a_step(in_place):
 
 
 # ------------------------------------------------------------------ out of range
+BAD = [dict(lens=-4, grow=1), dict(lens=-4, grow=40), dict(grow=-1), dict(grow=-2 ** 31), dict(held=-1), dict(held=5),
+       dict(held=2 ** 31 - 1), dict(held=5, release=1), dict(held=-3, release=1), dict(grow=-5, release=1),
+       dict(lens=-2, grow=-1), dict(lens=-2 ** 31, grow=2 ** 31 - 1)]
+
+
+@pytest.mark.parametrize("bad", BAD, ids=lambda x: ",".join(f"{k}={v}" for k, v in x.items()))
+@pytest.mark.parametrize("place", [0, 1, 2])
+def test_tables_leave_out_of_range_requests_as_they_are(bad, place):
+    """Such a request takes no page and gives none back; its length, its pages and its table
+    row stay (but new rows behind its committed pages have no page), its status is 3, and
+    the others go on as without it."""
+    wide, pages = 4, 16
+    lens, grow, held, release = [20, 5, 33], [7, 20, 2], [2, 1, 3], [0, 0, 0]
+    table = [[3, 4, 9, 9], [5, 9, 9, 9], [6, 7, 8, 9]]
+    free = [15, 14, 13, 12, 11]
+    for k, v in bad.items():
+        {"lens": lens, "grow": grow, "held": held, "release": release}[k][place] = v
+    ref = R.Tables(table, lens, held, free, PS)
+    rows = max(0, grow[place])
+    big = rows > 1000
+    use = [0 if b == place else grow[b] for b in range(3)]
+    ref.lens[place] = ref.held[place] = 0
+    slots, _, status = ref.step(use, [0] * 3, 0)
+    n_rows = 100
+    t, f = ints(table), ints(free + [-1] * 11)
+    r = jl.block_tables(ints(lens), ints(grow), t, ints(held), f, ints([5]), page_size=PS, num_pages=pages, n_rows=n_rows,
+                        release=ints(release))
+    with pytest.raises(jl.JetLongError, match="length|row count" if big else "length"):
+        jl.device_status()
+    jl.device_status()
+    status[place] = 3
+    assert r.status.tolist() == status
+    if lens[place] >= 0 and grow[place] > 0:
+        last = (lens[place] + grow[place] - 1) // PS
+        if last > (lens[place] - 1) // PS:
+            table[place][last] = jl.NO_PAGE
+    for b in range(3):
+        keep = b == place
+        assert int(r.lens[b]) == lens[b] and int(r.held[b]) == (held[b] if keep else ref.held[b])
+        assert t[b].tolist() == (table[b] if keep else ref.table[b])
+    n = int(r.free_count)
+    assert f[:n].tolist() == ref.free
+    # its token rows are counted and have no slot
+    if not big:
+        counts = [max(0, x) for x in grow]
+        assert r.row_start.tolist() == starts_of(counts)
+        want, it = [], iter(slots)
+        for b in range(3):
+            want += [-1] * counts[b] if b == place else [next(it) for _ in range(counts[b])]
+        assert r.slot_map.tolist() == want + [-1] * (n_rows - len(want))
+
+
 @pytest.mark.parametrize("page", [-1, 50, 2 ** 31 - 1, -2 ** 31])
 def test_commit_leaves_out_a_request_with_a_bad_page(page):
     """Rows that cannot be moved are not committed: the request stays as it was."""
