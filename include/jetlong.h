@@ -276,7 +276,8 @@ int jetlong_decode_noalloc(const void* q, const void* kcache, const void* vcache
  * free_list[0 .. *free_count) are the free pages (room for free_cap); pages are
  * taken from its end, in request order.  Pages given back by this call go onto
  * the list first (last request first, its last page first) and can be taken by
- * it.  Writes
+ * it.  A number that is no page, on the list or in a table row given back, is
+ * reported and passed on as JETLONG_NO_PAGE.  Writes
  *   status[b]     0 granted; 1 refused, the free pages end here (a request that
  *                 needs pages and comes after one is refused as well; one that
  *                 needs none is granted); 2 refused, longer than its table row.

@@ -194,12 +194,16 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
     if (gtid == 0 && carry.rows > p.n_rows) record_input(p.input_error, kBadRows);
     // pages given back: last request first, its last page first, so that pages
     // handed out together and given back together restore the list's order
-    const auto as_is = [](int page, int) { return page; };
+    const auto checked = [&](int page, int) {  // what is no page is handed on as none
+        if ((unsigned)page < (unsigned)p.num_pages) return page;
+        record_input(p.input_error, kBadPage);
+        return kNoPage;
+    };
     if ((long long)count + carry.back > p.free_cap && gtid == 0) record_input(p.input_error, kBadFreeList);
     each(0, carry.back, s_back, [&](int x, int b) {
         const long long at = (long long)count + (carry.back - s_back[b + 1]) + (s_back[b + 1] - 1 - x);
         return Move{p.table + (size_t)b * p.max_pages + (x - s_back[b]), at < p.free_cap ? p.free_list + at : nullptr, 0};
-    }, as_is);
+    }, checked);
     // from here on the old state may be overwritten, and the list holds every free page
     cluster_sync();
     const int avail = (int)min((long long)p.free_cap, (long long)count + carry.back);
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(TB_NT) block_tables_kernel(TablesProblem p)
     const int granted = s_need[bisect(s_need, p.B + 1, avail)];
     each(0, granted, s_need, [&](int x, int b) {
         return Move{p.free_list + (avail - 1 - x), p.table + (size_t)b * p.max_pages + s_held[b] + (x - s_need[b]), 0};
-    }, as_is);
+    }, checked);
     // the sums behind it are those of refused requests: their tables say so
     each(granted, s_need[p.B], s_need, [&](int x, int b) {
         return Move{nullptr, p.table + (size_t)b * p.max_pages + s_held[b] + (x - s_need[b]), 0};

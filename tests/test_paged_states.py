@@ -304,6 +304,27 @@ def test_tables_leave_out_of_range_requests_as_they_are(bad, place):
         assert r.slot_map.tolist() == want + [-1] * (n_rows - len(want))
 
 
+def test_pages_out_of_range_are_not_handed_on():
+    """A page number outside the pool, in a table row given back or in the free list, is
+    reported, and is nobody's page afterwards."""
+    import torch
+    bad = [99, -5, 2 ** 31 - 1]
+    for x in bad:
+        t, f = ints([[3, x, 4], [0, 0, 0]]), ints([7, 6, 0, 0, 0, 0, 0, 0])
+        r = jl.block_tables(ints([40, 0]), ints([0, 0]), t, ints([3, 0]), f, ints([2]), page_size=PS, num_pages=8, n_rows=0,
+                            release=ints([1, 0]))
+        with pytest.raises(jl.JetLongError, match="page number"):
+            jl.device_status()
+        assert int(r.free_count) == 5 and f[:5].tolist() == [7, 6, 4, jl.NO_PAGE, 3]
+    s = Server(2, 4, 8, free=[0, 1, 2, 99, 4])
+    s.kc.zero_(), s.vc.zero_()
+    r = s.tables([16, 20])  # pages 4, then 99 and 2
+    with pytest.raises(jl.JetLongError, match="page number"):
+        jl.device_status()
+    assert s.table.tolist()[1][:2] == [jl.NO_PAGE, 2] and s.table.tolist()[0][0] == 4
+    assert r.slot_map.tolist() == [64 + x for x in range(16)] + [-1] * 16 + [32 + x for x in range(4)]
+
+
 @pytest.mark.parametrize("page", [-1, 50, 2 ** 31 - 1, -2 ** 31])
 def test_commit_leaves_out_a_request_with_a_bad_page(page):
     """Rows that cannot be moved are not committed: the request stays as it was."""
