@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < NCOL; ++c) l[c] = 0.f;
             if (key < NCOL) {
-                nref[key] = -kNoRef;
+                nref[key] = key < ud->rows ? -kNoRef : 0.f;  // (a column without a query is no reason to move one)
                 zero[key] = 0.f;
             }
             if (named_or(bid, 128, !ok)) break;

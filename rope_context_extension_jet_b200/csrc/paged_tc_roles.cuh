@@ -670,12 +670,16 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                 }
             }
             if (setup) {
-                // rows without a query: logits times 0 whatever the tile holds, nothing attended
+                // Rows without a query: zeros, no drafted row attended.  (What shared memory held
+                // before must not decide whether the softmax moves its references: those of the
+                // other rows would move with them, and results change in their last bit.)
                 for (int row = rows + t; row < C::ROWS; row += C::ROTALL) {
                     lim0[row] = qG[row] = 0;
                     canc[row] = 0ull;
-                    cq[row] = 0.f;
+                    cq[row] = 1.f;
                 }
+                for (int x = rows * 2 * CH + t; x < C::ROWS * 2 * CH; x += C::ROTALL)
+                    *reinterpret_cast<uint4*>(smem + C::Q0 + C::q_off(x / (2 * CH), x % (2 * CH))) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -779,8 +783,9 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                     *pd = b1;
                 }
             } else {
-                // a request's last tiles: drafted rows sit at their depths (rows past the
-                // end: 0, they are masked)
+                // a request's last tiles: drafted rows sit at their depths.  Rows past the end
+                // are masked, and zeroed: large numbers there would have their neighbours
+                // scaled, and so rounded in another way.
                 if (!ro.wait(&bars.kfull[e % C::NKF], (e / C::NKF) & 1, 0x624)) { ok = false; break; }
 #pragma unroll 1
                 for (int x = 0; x < RPT; ++x) {
@@ -789,6 +794,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                     uint4* pa = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c));
                     uint4* pb = reinterpret_cast<uint4*>(kt + tc::sw128_off<KT>(r, c + CH));
                     uint4 a = *pa, b = *pb;
+                    if (j >= n) a = b = make_uint4(0u, 0u, 0u, 0u);
                     float ks = 1.f;
                     if (too_large(absmax8(a, b))) ks = scale_row(a, b);
                     if (c == 0) kscale[r] = ks;

@@ -167,3 +167,46 @@ def test_first_tiles_of_many_units(nodes, d):
     for _ in range(20):
         assert torch.equal(jl.decode_tree(*args, **kw), out)
     jl.device_status()
+
+
+@pytest.mark.parametrize("dtype,Hq,nodes", [("bf16", 32, 1), ("bf16", 24, 3), ("bf16", 32, 5), ("bf16", 32, 9), ("bf16", 32, 20),
+                                            ("bf16", 32, 33), ("bf16", 32, 50), ("fp32", 32, 1), ("fp32", 24, 3), ("fp32", 32, 5)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_results_do_not_depend_on_what_ran_before(dtype, Hq, nodes, d):
+    """Units with fewer rows than their kernel's tile has, and last tiles with fewer keys:
+    what an earlier kernel left in shared memory in their place (NaN, infinities, large and
+    small numbers) changes no bit."""
+    import torch
+    g = np.random.default_rng([Hq, nodes, d])
+    Hkv, T = 8, nodes
+    lens = [int(x) for x in g.integers(0, 400, 60)] + [2000, 1500, 0, 1]
+    wide = 2 + (2000 + T) // 16
+    num = sum(-(-(L + T) // 16) for L in lens) + 1
+    order, at = g.permutation(num), 0
+    table = np.zeros((len(lens), wide), np.int64)
+    for b, L in enumerate(lens):
+        p = -(-(L + T) // 16)
+        table[b, :p] = order[at:at + p]
+        at += p
+    rnd = lambda *s: torch.from_numpy(g.standard_normal(s, dtype=np.float32)).cuda().to(dt(dtype))
+    # logits that differ by tens of octaves, and elements that are subnormal in fp16
+    q, kc, vc = rnd(len(lens) * T, Hq, d), rnd(num, Hkv, 16, d), rnd(num, Hkv, 16, d)
+    kc *= (2.0 ** torch.randint(-16, 2, (num, Hkv, 16, 1), generator=torch.Generator().manual_seed(3))).cuda().to(kc.dtype)
+    args = (q, kc, vc, ints(table), ints(lens), ints([b * T for b in range(len(lens) + 1)]))
+    kw = dict(max_nodes=T, w0=100, w_pretrained=300, rope_theta=1e4, scale=4.0)
+    before = []
+    for value in (1.0, float("nan"), float("inf"), 3e38, -3e38, 1e-38, 0.0):
+        # every SM's shared memory full of it
+        x = torch.full((64 * 4, 32, d), value, device="cuda", dtype=dt(dtype))
+        c = torch.full((200, Hkv, 64, d), value, device="cuda", dtype=dt(dtype))
+        tab = ints(np.arange(200).reshape(4, 50))
+        run = lambda: jl.decode_tree(x, c, c, tab, ints([3100] * 4), ints([64 * b for b in range(5)]), max_nodes=64, w0=100,
+                                     w_pretrained=10000, rope_theta=1e4)
+        before.append(run)
+    out = jl.decode_tree(*args, **kw)
+    assert torch.isfinite(out).all()
+    for run in before:
+        for _ in range(3):
+            run()
+            assert torch.equal(jl.decode_tree(*args, **kw), out)
+    jl.device_status()
