@@ -35,7 +35,9 @@
  *     largest of their tensor lose relative precision, negligible in any
  *     logit); the decode scales each query head, and each key row of a key
  *     block whose unscaled logits would not be finite.  The scales are exact
- *     and undone in the softmax.  v: |v| below ~1e36 (P.V accumulates in fp32).
+ *     and undone in the softmax.  Their exponents end at +-100 in the prefill
+ *     and in the decode of contiguous caches, whose q and k must so stay below
+ *     2^115; the paged decode takes all of bf16.  v: |v| below ~1e36 (P.V accumulates in fp32).
  *     NaN inputs give NaN outputs.
  *   - All pointers named d_* or tensor pointers are DEVICE memory owned by the
  *     caller (jetlong_prefill_streamed also takes host buffers, named *_host).
@@ -340,11 +342,13 @@ int jetlong_decode_paged(const void* q, const void* kcache, const void* vcache, 
  * -- what jetlong_decode gives after its path has been committed.
  * Values in rows a node does not attend (non-finite ones too) do not reach it.
  * Requests may have no nodes; token rows outside every request, and those of
- * refused requests, are left as they were.  Without row_start (NULL) every request has one node, row b:
- * jetlong_decode_paged.
+ * refused requests, are left as they were.  Without row_start (NULL) every request
+ * has one node, row b: jetlong_decode_paged.
  * Two launches: the attention, cut into equal pieces over all requests whatever
- * their lengths, and a merge of the cut ones.  bf16 takes the input range of
- * jetlong_decode. */
+ * their lengths, and a merge of the cut ones.  bf16 takes any finite q and k whose
+ * logits are finite (scale up to 2^13).  A value that is not finite in a committed
+ * row, which every node attends, leaves its column of their outputs infinite or NaN
+ * where its weight is not 0. */
 size_t jetlong_decode_tree_workspace_size(int B, int Hq, int Hkv, int d, int max_nodes);
 int jetlong_decode_tree(const void* q, const void* kcache, const void* vcache, void* out, const int32_t* block_table,
                         const int32_t* lens, const int32_t* row_start, const int32_t* parents, int B, int N, int Hq,

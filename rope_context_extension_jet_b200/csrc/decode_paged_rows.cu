@@ -259,19 +259,21 @@ __global__ void __launch_bounds__(640, 1)
                                 x[32 + u] = __uint_as_float(t1[u]);
                             }
                         }
-                        // key rows that were scaled by a power of two (paged_tc_roles.cuh) scaled back
+                        // key rows that were scaled by a power of two (paged_tc_roles.cuh): the
+                        // whole factor here, in place of cq
                         if (any_scaled) {
                             asm volatile("" ::: "memory");
                             const float4* k4 = reinterpret_cast<const float4*>(ksc + (e % INFO) * KT + h * 64);
 #pragma unroll
                             for (int u = 0; u < KT / 2; u += 4) {
                                 const float4 f = k4[u / 4];
-                                x[u] *= f.x;
-                                x[u + 1] *= f.y;
-                                x[u + 2] *= f.z;
-                                x[u + 3] *= f.w;
+                                x[u] *= logit_factor(cq, f.x);
+                                x[u + 1] *= logit_factor(cq, f.y);
+                                x[u + 2] *= logit_factor(cq, f.z);
+                                x[u + 3] *= logit_factor(cq, f.w);
                             }
                         }
+                        const float cf = any_scaled ? 1.f : cq;
                         // what does not belong to this row and item at -inf
                         if (masked) {
                             asm volatile("" ::: "memory");  // a branch, not predication: most tiles skip this
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(640, 1)
                                 }
                             }
                             const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                            // logits in log2 units: x cq, cq > 0 a power of two times the scale;
+                            // logits in log2 units: x cf, cf > 0 a power of two times the scale;
                             // both halves of the row's keys follow.  One place per stream: a
                             // unit's first two tasks come here without an agreement between them,
                             // so the other warp may already write the second task's maximum while
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(640, 1)
                             float* const mine = tops + (s * 2 + h) * 128 + lrow;
                             *mine = top;
                             named_sync(pid, 64);
-                            const float mt = fmaxf(top, mine[h ? -128 : 128]) * cq;
+                            const float mt = fmaxf(top, mine[h ? -128 : 128]) * cf;
                             // (64 weights that sum to more than 2^kExceed hold one above 2^(kExceed - 6))
                             const bool resc = mt > ref + (kExceed - 6.5f);
                             float alpha = 1.f;
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(640, 1)
                                 tmem_wait_st();
                             }
                         }
-                        const float2 sl = make_float2(cq, cq), nm = make_float2(-ref, -ref);
+                        const float2 sl = make_float2(cf, cf), nm = make_float2(-ref, -ref);
                         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int u = 0; u < KT / 2; u += 4) {

@@ -61,8 +61,8 @@ struct CfgTiles {
 template <int D, int NCOL>
 struct Cfg : CfgTiles<D, NCOL>,
              Notes<D, NCOL, CfgTiles<D, NCOL>::NSK, CfgTiles<D, NCOL>::NSV, CfgTiles<D, NCOL>::BASE, 6, 16> {
-    static constexpr int M0 = Cfg::NOTES_END;               // [NCOL] minus the column references, [NCOL] zeros
-    static constexpr int RED = M0 + NCOL * 8;               // [4][NCOL] column maxima / sums, [NCOL] rescale factors
+    static constexpr int M0 = Cfg::NOTES_END;               // [NCOL] minus the column references, [NCOL] zeros, [NCOL] ones
+    static constexpr int RED = M0 + NCOL * 12;              // [4][NCOL] column maxima / sums, [NCOL] rescale factors
     static constexpr int TOTAL = RED + 5 * NCOL * 4 + 1024;
     static_assert(TOTAL <= 232448, "shared memory");
 };
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
         const float* ksc = reinterpret_cast<const float*>(smem + C::KSC);
         const uint32_t tl = tmem + ((uint32_t)(32 * wl) << 16);
         float* nref = reinterpret_cast<float*>(smem + C::M0);
-        float* zero = nref + NCOL;
+        float *zero = nref + NCOL, *one = zero + NCOL;
         float* red = reinterpret_cast<float*>(smem + C::RED);
         float* alpha = red + 4 * NCOL;
         float l[NCOL];  // sums over this thread's keys
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
             if (key < NCOL) {
                 nref[key] = key < ud->rows ? -kNoRef : 0.f;  // (a column without a query is no reason to move one)
                 zero[key] = 0.f;
+                one[key] = 1.f;
             }
             if (named_or(bid, 128, !ok)) break;
             const int cols = ud->rows, L = ud->L, n = L + ud->T;
@@ -262,18 +263,19 @@ __global__ void __launch_bounds__(Cfg<D, NCOL>::THREADS, 1)
 #pragma unroll
                         for (int c = 0; c < NCOL; ++c) y[c] = __uint_as_float(raw[c]);
                     }
-                    if (any_scaled) {
+                    if (any_scaled) {  // the whole factor here, 1 below
                         asm volatile("" ::: "memory");
 #pragma unroll
-                        for (int c = 0; c < NCOL; ++c) y[c] *= ks;
+                        for (int c = 0; c < NCOL; ++c) y[c] *= logit_factor(cq[c], ks);
                     }
+                    const float* factor = any_scaled ? one : cq;
 #pragma unroll
                     for (int cb = 0; cb < NCOL; cb += 16) {
                         if (cb < cols) {
                             asm volatile("" ::: "memory");  // scales of 16 columns at a time: registers
 #pragma unroll
                             for (int c = cb; c < cb + 16; c += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4*>(cq + c);
+                                const float4 k4 = *reinterpret_cast<const float4*>(factor + c);
                                 const float4 m4 = *reinterpret_cast<const float4*>(nm + c);
                                 const float2 a = fma2(make_float2(y[c], y[c + 1]), make_float2(k4.x, k4.y), make_float2(m4.x, m4.y));
                                 const float2 b = fma2(make_float2(y[c + 2], y[c + 3]), make_float2(k4.z, k4.w), make_float2(m4.z, m4.w));

@@ -256,6 +256,19 @@ __device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b)
 }
 __device__ __forceinline__ uint32_t mag16(uint32_t a) { return max(a & 0x7fffu, (a >> 16) & 0x7fffu); }
 
+// Exponent of the power of two that brings a row's largest element into [2^13, 2^14)
+// (at most 2^126, for subnormals); rows of zeros, or with infinities or NaN, stay.
+__device__ __forceinline__ int row_exp(uint32_t mag)
+{
+    if (mag == 0u || mag >= 0x7f80u) return 0;
+    return min(126, 140 - max((int)(mag >> 7), 1));
+}
+
+// Factor of a logit whose key row was scaled: that of its query row (cq) times the inverse
+// key scale, formed first, since a raw logit times either alone can be outside fp32 where
+// the logit is not.  (Too large a factor belongs to an infinite logit, or to a raw one of 0.)
+__device__ __forceinline__ float logit_factor(float cq, float ks) { return fminf(cq * ks, 3.40282347e38f); }
+
 // What every role sees.
 template <class C>
 struct Role {
@@ -610,7 +623,8 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
             uint32_t mx = mag16(absmax8(lo, hi));
 #pragma unroll
             for (int o = 1; o < CH; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int ex = tc::range_exp(mx);
+            // (cq stays a normal number; logits of smaller queries are below 2^-4)
+            const int ex = min(row_exp(mx), (int)(__float_as_uint(p.scale_log2) >> 23) - 1);
             const float sc = tc::pow2i(ex);
             if (setup) {
                 float l1 = sum8(lo) + sum8(hi);
@@ -731,7 +745,7 @@ __device__ __forceinline__ void rotate_keys(const Role<C>& ro)
                 uint32_t m = mag16(absmax8(lo, hi));
 #pragma unroll
                 for (int o = 1; o < CH; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const int ex = tc::range_exp(m);
+                const int ex = row_exp(m);
                 scale8(lo, tc::pow2i(ex));
                 scale8(hi, tc::pow2i(ex));
                 scaled = 1;
