@@ -79,6 +79,7 @@ PREFILL_SOURCES = ("prefill_pair.cu", "prefill_tc_common.cuh", "tc_ptx.cuh", "jl
 
 
 DECODE_SOURCES = ("decode.cu", "jl_ptx.cuh", "jl_common.cuh")
+PAGED_SOURCES = ("paged_common.cuh", "prefill_tc_common.cuh", "tc_ptx.cuh", "jl_ptx.cuh", "jl_common.cuh")
 
 
 def prefill_source_hash(names=PREFILL_SOURCES):
@@ -320,6 +321,20 @@ def run_profile(args):
         for _ in range(args.warmup + args.steps):
             jl.prefill(q, k, v, out, w0=w.w0, w_pretrained=w.w_pretrained,
                        rope_theta=w.rope_theta, scale=w.scale)
+    elif args.profile in PAGED:
+        _, _, B, T, dtype = PAGED[args.profile]
+        g, el, ps = torch.Generator(device="cuda").manual_seed(1), getattr(torch, dtype), 64
+        pages = -(-(args.L + T) // ps)
+        kc, vc = (torch.randn((B * pages, I.D.Hkv, ps, I.D.d), generator=g, device="cuda").to(el) for _ in range(2))
+        table = torch.randperm(B * pages, generator=g, device="cuda").to(torch.int32).view(B, pages)
+        q = torch.randn((B * T, I.D.Hq, I.D.d), generator=g, device="cuda").to(el)
+        lens = torch.full((B,), args.L, dtype=torch.int32, device="cuda")
+        starts = torch.arange(0, B * T + 1, T, dtype=torch.int32, device="cuda")
+        # a binary tree: node t hangs on (t - 1) / 2
+        parents = torch.tensor([-1] + [(t - 1) // 2 for t in range(1, T)], dtype=torch.int32).cuda().repeat(B)
+        for _ in range(args.warmup + args.steps):
+            jl.decode_tree(q, kc, vc, table, lens, starts, parents, max_nodes=T, w0=I.D.w0,
+                           w_pretrained=I.D.w_pretrained, rope_theta=I.D.rope_theta)
     else:
         w = I.D.with_(L0=args.L - 1, Lcap=args.L + 64, steps=1)
         qs, kc, vc = I.decode_inputs(w)
@@ -350,6 +365,12 @@ NCU_METRICS = (
     "smsp__inst_executed.sum",
 )
 NCU_KERNELS = {"prefill": "prefill_pair_kernel", "decode": "decode_tc_kernel"}
+# Paged decode: (kernel, its source, requests, nodes of each one's tree, element type).
+PAGED = {"paged-row": ("decode_paged_tc_kernel", ("decode_paged_tc.cu", "paged_tc_roles.cuh"), 4, 1, "bfloat16"),
+         "paged-tree8": ("decode_paged_tc_kernel", ("decode_paged_tc.cu", "paged_tc_roles.cuh"), 2, 8, "bfloat16"),
+         "paged-tree64": ("decode_paged_rows_kernel", ("decode_paged_rows.cu", "paged_tc_roles.cuh"), 2, 64, "bfloat16"),
+         "paged-fp32": ("decode_paged_fp32_kernel", ("decode_paged_fp32.cu",), 4, 1, "float32")}
+NCU_KERNELS.update({mode: p[0] for mode, p in PAGED.items()})
 
 
 def parse_ncu_csv(text):
@@ -437,13 +458,16 @@ def _ncu_cmd(extra, bench_args, log):
 
 # Every capture profiles/ holds, in the order they run: (mode, L).
 NCU_ALL = (("launches", None), ("traffic", 131072), ("prefill", 32768), ("decode", 32768),
-           ("prefill-full", 32768), ("decode-full", 32768))
+           ("prefill-full", 32768), ("decode-full", 32768), ("paged-row", 65536), ("paged-tree8", 65536),
+           ("paged-tree64", 65536), ("paged-fp32", 16384))
 
 
 def ncu_summary_name(mode, L):
     """File name (without extension) under profiles/ of the capture `mode` at length L."""
     if mode == "launches":
         return "launches_bench"
+    if mode in PAGED:
+        return f"{PAGED[mode][0]}_T{PAGED[mode][3]}_L{L}_counters"
     kname = NCU_KERNELS["decode" if mode.startswith("decode") else "prefill"]
     if mode == "traffic":
         return f"{kname}_L{L}_dram"
@@ -529,6 +553,12 @@ def run_ncu(args):
                         "tflops": computed / dur / 1e12 if dur > 0 else None})
             rec["frac_of_bf16_burst"] = rec["tflops"] / peaks["bf16_tflops"] if rec["tflops"] else None
             kname = NCU_KERNELS["prefill"]
+        elif args.ncu in PAGED:
+            kname, _, B, T, dtype = PAGED[args.ncu]
+            kv = 2 * B * (args.L + T) * I.D.Hkv * I.D.d * (2 if dtype == "bfloat16" else 4)
+            rec.update({"workload": f"paged decode {dtype} B={B} nodes={T} Hq={I.D.Hq} Hkv={I.D.Hkv} d={I.D.d} L={args.L}",
+                        "kv_bytes": kv, "gbs_kv": kv / dur / 1e9 if dur > 0 else None})
+            rec["frac_of_hbm"] = rec["gbs_kv"] / peaks["hbm_gbs"] if rec["gbs_kv"] else None
         else:
             w = I.D.with_(L0=args.L - 1, Lcap=args.L + 64, steps=1)
             kv, allb = decode_bytes(w, args.L)
@@ -552,6 +582,8 @@ def run_ncu(args):
                           f"{rec['frac_of_hbm']:.3f} of the {peaks['source']} HBM copy bandwidth "
                           f"({peaks['hbm_gbs']} GB/s); DRAM counted {dram / 1e9:.3f} GB."]
     srcs = DECODE_SOURCES if args.ncu.startswith("decode") else PREFILL_SOURCES
+    if args.ncu in PAGED:
+        srcs = PAGED[args.ncu][1] + PAGED_SOURCES
     if args.ncu == "launches":
         srcs = PREFILL_SOURCES + ("decode.cu", "range_scan.cu", "rope_keys.cu")
     lines += ["", f"Sources: sha256 of {', '.join(srcs)}: {prefill_source_hash(srcs)[:16]}; "
@@ -585,14 +617,14 @@ def main():
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--cpu-budget", type=float, default=20.0)
-    ap.add_argument("--profile", choices=["prefill", "decode"], default=None,
+    ap.add_argument("--profile", choices=["prefill", "decode", *PAGED], default=None,
                     help="run only one kernel on a reduced workload (for ncu captures)")
     ap.add_argument("--L", type=int, default=32768, help="sequence / cache length for --profile")
     ap.add_argument("--ncu", choices=["launches", "prefill", "decode", "traffic", "prefill-full", "decode-full",
-                                      "all"],
+                                      *PAGED, "all"],
                     default=None,
                     help="profiling harness: the bench command (launches), one kernel of the --profile "
-                         "workloads (prefill, decode) or one full-size prefill's DRAM bytes (traffic, "
+                         "workloads (prefill, decode, paged-...) or one full-size prefill's DRAM bytes (traffic, "
                          "--L 131072), under ncu; writes the summary (.md) and its figures (.json) under "
                          "profiles/; 'all' runs every capture profiles/ holds, one after the other")
     args = ap.parse_args()
