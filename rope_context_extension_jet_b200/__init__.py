@@ -487,7 +487,9 @@ def block_tables(lens, grow, block_table, held, free_list, free_count, *, page_s
                  status=None, stream=None) -> BlockTables:
     """Make room for grow[b] new rows of every request and map them to slots
     (jetlong_block_tables).  ``block_table`` [B, max_pages] and ``free_list`` are
-    updated in place; the ``*_out`` arrays may be their inputs."""
+    updated in place; the ``*_out`` arrays may be their inputs.  A refused request's
+    table gets NO_PAGE where its new rows would be, by which the other calls leave it
+    out; a place with lens[b] < 0 and grow[b] == 0 is idle."""
     import torch
     if block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("block_table must be [B, max_pages] and free_list one-dimensional")
@@ -572,7 +574,10 @@ def decode_tree(q, kcache, vcache, block_table, lens, row_start, parents=None, o
     """Decode a tree of drafted rows per request: raw q [N, Hq, d], request b's
     nodes in token rows [row_start[b], row_start[b + 1]), parents [N] within each
     request (-1: the last committed row; None: chains), node t appended as row
-    lens[b] + t (jetlong_decode_tree)."""
+    lens[b] + t (jetlong_decode_tree).  Rows of ``out`` of requests without nodes and
+    of refused ones are left as they were.  The kernel follows max_nodes, not the
+    nodes of the call: what it holds per unit (at 64 nodes of 4 heads 256 query rows)
+    costs time also where only a few of them are used."""
     import torch
     num_pages, Hkv, page_size, d = _paged_shapes(q, kcache, vcache, block_table)
     N, Hq, _ = q.shape
@@ -602,8 +607,8 @@ def decode_tree(q, kcache, vcache, block_table, lens, row_start, parents=None, o
 def tree_commit(kcache, vcache, block_table, lens, row_start, parents, last, *, max_nodes: int, lens_out=None,
                 n_accepted=None, stream=None):
     """Commit the path to node last[b] (-1: none) of every request: its rows
-    become rows lens[b], lens[b] + 1, ... and lens_out = lens + their number
-    (jetlong_tree_commit).  Returns (lens_out, n_accepted)."""
+    become rows lens[b], lens[b] + 1, ... and lens_out = lens + their number; refused
+    and idle ones stay as they are (jetlong_tree_commit).  Returns (lens_out, n_accepted)."""
     import torch
     num_pages, Hkv, page_size, d = _caches(kcache, vcache)
     if block_table.dim() != 2 or row_start.dim() != 1:

@@ -18,10 +18,13 @@
 // A unit of RT = R WR rows puts WR warps on every tile (a row group each) and spreads
 // tiles over 8 / WR key groups; their states are joined where the unit ends.
 //
-// Bound: HBM up to 8 rows, fp32 arithmetic above (256 FMA per key and row at d = 128).
-// Measured, 32 query heads on 8, d = 128: 8 requests of 16,000 rows 178 us (5.9 TB/s of
-// K and V), trees of 8 nodes on them 643 us.  (Without the next batch's logits beside
-// this one's values 213 and 865 us; keys and values staged by plain loads 567 and 2310.)
+// Bound: HBM up to 8 rows.  Measured, 32 query heads on 8, d = 128: 8 requests of 16,000
+// rows 178 us (5.9 TB/s of K and V).  With more rows it is far from either bound: trees
+// of 8 nodes on them 660-720 us, where the 256 FMA per key and row take 235.  Each row
+// group of a unit turns every key again, and each (key, row) costs a shuffle for its
+// weight and its part of the exchange of the dots.  (Without the next batch's logits
+// beside this one's values 213 and 865 us; keys and values staged by plain loads 567
+// and 2310.)
 #include <algorithm>
 
 #include "paged_common.cuh"

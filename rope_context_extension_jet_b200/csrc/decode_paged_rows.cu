@@ -24,9 +24,13 @@
 // made from: the weights in columns 0-31, what they leave of 16 bits in 32-47), O_0,
 // O_1.
 //
-// Bound: the softmax (8 x 32K rows: 16 nodes 247 us, 64 nodes 451 us; 64 nodes at 8 x
-// 128K 1.67-1.78 ms, where bytes and products each take 0.66 ms).  Exponentials on the
-// FMA pipes made it slower (an eighth of them 6%): instruction issue, not MUFU, is short.
+// Bound: latencies in the softmax (8 x 32K rows: 16 nodes 261 us, 64 nodes 471 us; 64
+// nodes at 8 x 128K 1.72-1.87 ms, where bytes and products each take 0.66 ms).  A tile of
+// 256 rows takes about 5500 cycles, of which the exponentials need 2048 and the products
+// 2560, with half of the issue slots empty: a thread loads all of its 64 scores before
+// the first exponential, and the wait for S and the agreement of the two warps that
+// share rows stand beside that.  Exponentials on the FMA pipes made it slower (an eighth
+// of them 6%).
 #include <algorithm>
 
 #include "paged_tc_roles.cuh"
@@ -74,7 +78,8 @@ __global__ void __launch_bounds__(640, 1)
     // decode_paged_tc.cu, each costs a product and the softmax's time.  128K trees of 64
     // nodes, with the row maximum still taken on every tile: error 2.4e-3 (rms, of the
     // results) and 1779 us with none, 2.2e-3 and 1939 us with one of the two, 1.9e-3 and
-    // 2238 us with both; rounding the results alone is 1.6e-3.
+    // 2238 us with both; rounding the results alone is 1.6e-3.  (So a row is less exact
+    // here than in decode_paged_tc.cu, which keeps both terms.)
     constexpr int PARTS = 1;
     constexpr float kSumMax = 65536.f;  // 2^kExceed
     static_assert(kExceed == 16.f && PARTS == 1, "weights");

@@ -27,9 +27,10 @@
 //   warps 12-.. softmax, one warpgroup per NCOL columns
 // Every wait on a barrier is bounded as in the prefill kernels.
 //
-// Bound: HBM at 128K (8 requests, 32 query heads on 8, d = 128: 664-757 us on different
-// boxes, 5.7-6.5 TB/s of K and V); the rotation of the key tiles where there are more
-// rows or phases (8 x 32K: 4 nodes 185 us, 8 nodes 234 us; bytes alone 162 us).
+// Bound: HBM at 128K (8 requests, 32 query heads on 8, d = 128: 649-660 us one call right
+// after another, 6.5 TB/s of K and V, 800 where every call has another cache); the
+// rotation of the key tiles where there are more rows or phases (8 x 32K: 4 nodes 189 us,
+// 8 nodes 242 us; bytes alone 162 us).
 #include <algorithm>
 
 #include "paged_tc_roles.cuh"
